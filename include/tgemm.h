@@ -56,7 +56,11 @@
 extern "C" {
 #endif
 
-typedef enum { TGEMM_F16 = 0, TGEMM_BF16 = 1 } tgemm_dtype;
+typedef enum {
+    TGEMM_F16 = 0,
+    TGEMM_BF16 = 1,
+    TGEMM_F32 = 2 /* logits of moe_route and moe_route_backward only */
+} tgemm_dtype;
 
 typedef enum {
     TGEMM_B_NK = 0, /* B is [N,K], K contiguous: C = A x B^T */
@@ -316,6 +320,198 @@ int tgemm_workspace_size(int64_t m, int64_t n, const tgemm_config* cfg, int64_t*
  */
 int attn_fwd_f16(int64_t batch, int64_t seq, int64_t heads, int64_t dim, const void* Q,
                  const void* K, const void* V, void* O, int causal, void* stream);
+
+/*
+ * ---- Products with an epilogue ------------------------------------------------------
+ *
+ *   z[m,n] = sum_k a(m,k) b(n,k) + bias[n]
+ *   C[m,n] = act(z[m,n]) + residual[m,n]                            n < N
+ *   C[m,n] = act(z[m,n]) * z[m, n + N/2] + residual[m,n]            n < N/2, gated
+ *
+ * in fp32 up to one rounding of C (and of z, where it is kept).  The conventions of the
+ * products hold (ownership, asynchrony, errors, thread safety), with these differences:
+ *   - sizes and leading dimensions are below 2^31; no product of them is bounded (C may
+ *     span more than 2^31 elements);
+ *   - any 2-byte alignment, size and leading dimension is accepted; the fast kernels need
+ *     A and B 16-byte aligned, lda and ldb multiples of 8, K a multiple of 8 (with B
+ *     [K,N]: N, and gated N/2, as well) and B (one group's) within 2^31 bytes;
+ *   - K == 0 gives z = bias.
+ */
+typedef enum {
+    TGEMM_ACT_NONE = 0,      /* z                                                     */
+    TGEMM_ACT_RELU = 1,      /* max(z, 0); slope 0 at 0                               */
+    TGEMM_ACT_GELU = 2,      /* z Phi(z), Phi the normal distribution function         */
+    TGEMM_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2        */
+    TGEMM_ACT_SILU = 4       /* z / (1 + exp(-z))                                      */
+} tgemm_activation;
+
+/* What follows the sums.  A zeroed structure (or NULL in its place) adds nothing. */
+typedef struct {
+    int32_t activation;   /* tgemm_activation                                          */
+    int32_t gated;        /* 1: N is even, and C has N/2 columns                       */
+    const void* bias;     /* N values of the operands' type, or NULL                   */
+    int64_t bias_stride;  /* gemm_grouped: elements between two groups' biases         */
+    const void* residual; /* of C's size, row stride ldr, or NULL; may be C itself     */
+    int64_t ldr;
+    void* preact;         /* takes z, N columns, row stride ldp, or NULL               */
+    int64_t ldp;
+} tgemm_epilogue;
+
+/*
+ * The product with an epilogue: A [m,k], B per b_layout, C [m, n] (gated: [m, n/2]).
+ *   lda, ldb, ldc : leading dimensions in elements
+ *   epilogue      : NULL for none
+ * preact keeps z for gemm_fused_backward.  residual may be C (same address and stride:
+ * C += act(z)); any other overlap of C or preact with another tensor is
+ * TGEMM_ERR_ALIASING.  Errors as gemm_strided.
+ */
+int gemm_fused(int dtype, int64_t m, int64_t n, int64_t k, const void* A, int64_t lda,
+               const void* B, int64_t ldb, int b_layout, void* C, int64_t ldc,
+               const tgemm_epilogue* epilogue, void* stream);
+
+/*
+ * Its gradients for dC [m, n] (gated: [m, n/2]):
+ *   dZ = dC act'(z), or gated [dC u act'(g) | dC act(g)] with z = [g | u]
+ *   dA = dZ b^T [m,k];  dB = dZ^T a, stored as B is;  dbias[n] = sum_m dZ[m,n], fp32
+ * (the residual's gradient is dC itself).  dA, dB and dbias may each be NULL (not wanted).
+ *   preact     : z as gemm_fused kept it; not read without an activation and a gate
+ *   dZ         : takes dZ, [m,n] of the operands' type, row stride lddz: the two products
+ *                read it, so it is rounded once to their type; may be preact itself (same
+ *                address and stride).  Not used without an activation and a gate, nor when
+ *                neither dA nor dB is wanted
+ *   dbias      : from the unrounded dZ, summed in a fixed order
+ *   workspace  : needed with dbias, gemm_backward_workspace_size(1, m, n) bytes, 16-byte
+ *                aligned; else ignored
+ * Errors as gemm_fused, and TGEMM_ERR_WORKSPACE.
+ */
+int gemm_fused_backward(int dtype, int64_t m, int64_t n, int64_t k, const void* dC,
+                        int64_t lddc, const void* A, int64_t lda, const void* B, int64_t ldb,
+                        int b_layout, int activation, int gated, const void* preact,
+                        int64_t ldp, void* dZ, int64_t lddz, void* dA, int64_t ldda, void* dB,
+                        int64_t lddb, float* dbias, void* workspace, int64_t workspace_bytes,
+                        void* stream);
+
+/* Workspace bytes of gemm_fused_backward (groups 1) and gemm_grouped_backward with dbias.
+ * Host-only. */
+int gemm_backward_workspace_size(int64_t groups, int64_t rows, int64_t n, int64_t* bytes);
+
+/*
+ * One product per group of rows, each with its own B (and bias), as the experts of a
+ * mixture take them: for every group g and every row s of C in
+ * offsets[g] .. offsets[g+1]-1
+ *   C[s] = epilogue_g( sum_k A[r(s), k] b_g(n,k) ),   r(s) = row_index[s] / row_div
+ * (r(s) = s where row_index is NULL).
+ *   groups    : 1 .. 65535
+ *   rows      : rows of C, and of preact, residual and row_index
+ *   offsets   : device pointer, groups + 1 int32, ascending; read by the kernels only.  An
+ *               offset outside 0 .. rows counts as the nearer end, and a group whose end
+ *               lies before its start is empty
+ *   row_index : device pointer, rows int32, or NULL; an index outside A's a_rows rows
+ *               (after the division) stands for a row of zeros
+ *   row_div   : >= 1; with moe_plan's order and row_div = k, each row reads its token's
+ *               row of A in place
+ *   stride_b  : elements between two groups' B (0: one B for all)
+ *   epilogue  : bias per group, bias_stride elements apart
+ * Rows of C and preact outside every group are left as they were.  Errors as gemm_fused.
+ */
+int gemm_grouped(int dtype, int64_t groups, int64_t rows, int64_t n, int64_t k,
+                 const int32_t* offsets, const int32_t* row_index, int64_t row_div,
+                 const void* A, int64_t a_rows, int64_t lda, const void* B, int64_t ldb,
+                 int64_t stride_b, int b_layout, void* C, int64_t ldc,
+                 const tgemm_epilogue* epilogue, void* stream);
+
+/*
+ * Its gradients, per row and per group: dA[s] = dZ[s] b_g^T, one row per row of C (with a
+ * row index the gradients of a shared row of A are the sums of its rows' dA, which
+ * moe_combine without weights adds up); dB and dbias per group, stride_db elements and n
+ * floats apart, an empty group's being zero.  Rows of dZ and dA outside every group are
+ * left as they were.  Everything else as for gemm_fused_backward and gemm_grouped.
+ */
+int gemm_grouped_backward(int dtype, int64_t groups, int64_t rows, int64_t n, int64_t k,
+                          const int32_t* offsets, const int32_t* row_index, int64_t row_div,
+                          const void* dC, int64_t lddc, const void* A, int64_t a_rows,
+                          int64_t lda, const void* B, int64_t ldb, int64_t stride_b,
+                          int b_layout, int activation, int gated, const void* preact,
+                          int64_t ldp, void* dZ, int64_t lddz, void* dA, int64_t ldda,
+                          void* dB, int64_t lddb, int64_t stride_db, float* dbias,
+                          void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * ---- Routing to experts --------------------------------------------------------------
+ */
+typedef enum { TGEMM_SCORE_SOFTMAX = 0, TGEMM_SCORE_SIGMOID = 1 } tgemm_scoring;
+typedef enum {
+    TGEMM_GROUP_MAX = 0, /* a group's score is its largest selection value             */
+    TGEMM_GROUP_TOP2 = 1 /* the sum of its two largest (of one, where it has one)      */
+} tgemm_group_score;
+
+/*
+ * The k experts of every token and their weights, from logits [tokens, experts]:
+ *   s = softmax(logits) or 1 / (1 + exp(-logits)), selection values c = s + bias;
+ *   with topk_groups < groups, only the experts of the topk_groups groups (of
+ *   experts / groups consecutive experts) with the highest scores; then the k experts of
+ *   largest c, in that order, the lowest index first among equal values.
+ *   weights = s of the chosen (without the bias), divided by their sum if renormalize is
+ *   1, times scale.
+ * Without a bias and a choice of groups the experts are ordered by their logits.  With
+ * either, c is computed in fp64, so that near scores are told apart.  A logit of -infinity
+ * or NaN, or a NaN c, or a c of -infinity, is never chosen; +infinity counts as the
+ * largest finite value.  Choices beyond the candidates (all of them, for a token whose
+ * logits are all masked) get id -1 and weight 0.
+ *   logits_dtype : TGEMM_F16, TGEMM_BF16 or TGEMM_F32
+ *   experts      : 1 .. 1024;  k : 1 .. min(experts, 64)
+ *   ldx          : row stride of the logits (>= experts)
+ *   bias         : experts floats, or NULL
+ *   groups       : divides experts, at most 64; topk_groups : 1 .. groups
+ *   ids, weights : [tokens, k] int32 and fp32, packed
+ * Returns a tgemm_status; tokens == 0 is a no-op.
+ */
+int moe_route(int logits_dtype, int64_t tokens, int64_t experts, int64_t k,
+              const void* logits, int64_t ldx, const float* bias, int scoring, int64_t groups,
+              int64_t topk_groups, int group_score, int renormalize, float scale,
+              int32_t* ids, float* weights, void* stream);
+
+/* The logits' gradient [tokens, experts] (of the logits' type) from the weights' gradient
+ * [tokens, k] fp32, for the given choices (distinct per token; ids outside the experts are
+ * passed over).  scoring, renormalize and scale as in the forward call. */
+int moe_route_backward(int logits_dtype, int64_t tokens, int64_t experts, int64_t k,
+                       const void* logits, int64_t ldx, const int32_t* ids,
+                       const float* dweights, int scoring, int renormalize, float scale,
+                       void* dlogits, int64_t lddx, void* stream);
+
+/*
+ * The plan of a step: its choices (ids of all tokens in order, tokens * k of them) sorted
+ * by expert, equal experts in the order of the choices.
+ *   offsets : [experts + 1]; expert e has the rows offsets[e] .. offsets[e+1]-1
+ *   order   : [choices]; the choice behind each row, -1 past the last row
+ *   slots   : [choices]; the row of each choice, -1 for an id outside the experts
+ *   experts : 1 .. 1024;  choices : < 2^31
+ *   workspace : moe_plan_workspace_size bytes, 4-byte aligned (0 bytes up to 4096 choices)
+ * offsets goes to gemm_grouped, order to its row_index (with row_div = k), slots to
+ * moe_combine.
+ */
+int moe_plan(int64_t choices, int64_t experts, const int32_t* ids, int32_t* offsets,
+             int32_t* order, int32_t* slots, void* workspace, int64_t workspace_bytes,
+             void* stream);
+int moe_plan_workspace_size(int64_t choices, int64_t experts, int64_t* bytes);
+
+/*
+ * Y[t] = residual[t] + sum_j weights[t,j] O[slots[t,j]], j < k, in fp32, rounded once.
+ *   O        : [rows, width] fp16 or bf16, row stride ldo;  slots : [tokens, k]; a slot
+ *              outside 0 .. rows-1 adds nothing
+ *   weights  : [tokens, k] fp32, or NULL (all one);  residual : or NULL; may be Y itself
+ */
+int moe_combine(int dtype, int64_t tokens, int64_t k, int64_t width, const void* O,
+                int64_t rows, int64_t ldo, const int32_t* slots, const float* weights,
+                const void* residual, int64_t ldr, void* Y, int64_t ldy, void* stream);
+
+/* Its gradients: dO[slots[t,j]] = weights[t,j] dY[t] (rows no choice names are left as they
+ * were; each row is to be named at most once) and dweights[t,j] = <dY[t], O[slots[t,j]]>
+ * (0 without a row).  dO or dweights may be NULL; O is read for dweights only. */
+int moe_combine_backward(int dtype, int64_t tokens, int64_t k, int64_t width, const void* dY,
+                         int64_t lddy, const void* O, int64_t rows, int64_t ldo,
+                         const int32_t* slots, const float* weights, void* dO, int64_t lddo,
+                         float* dweights, void* stream);
 
 /*
  * Diagnostics for measurements: clock stamps on every compute unit.  Engine cycles are

@@ -1,0 +1,595 @@
+// gfx950 kernels of the products with an epilogue (gemm_fused) and of the products over
+// ragged groups of rows (gemm_grouped), forward and backward.
+//
+//   z[s,n] = sum_k a(s,k) b_g(n,k) + bias_g[n]          s a row of group g
+//   C[s,n] = act(z[s,n]) + residual[s,n]                 or, gated, with h = N / 2,
+//   C[s,n] = act(z[s,n]) * z[s,n+h] + residual[s,n]      n < h
+//
+// A plain product is one group of all rows.  Groups are runs of rows of C (and of A, or of
+// an index into A) between consecutive offsets, which lie in device memory: the host does
+// not know them, launches the most tiles that any offsets could need, and each workgroup
+// finds its tile by a prefix sum over the groups' tile counts.  Everything up to the one
+// rounding of C (and of z, where it is kept for the backward pass) is fp32.
+#pragma once
+
+#include "kernels.hpp"
+
+namespace tgemm {
+
+enum { ACT_NONE = 0, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU };
+
+// One call, as the kernels see it.  Sizes fit 32 bits; rows times a leading dimension may
+// not, and is computed in 64.
+struct FusedArgs {
+    const u16* A;
+    const u16* B;
+    u16* C;
+    const u16* bias;       // [N] per group, or null
+    const u16* residual;   // rows of C's width, or null; may be C itself
+    u16* preact;           // rows of N, or null
+    const int32_t* offsets;    // [groups + 1], or null: one group of all rows
+    const int32_t* row_index;  // row s of the product is row row_index[s] / row_div of A
+    int64_t stride_b, stride_c, stride_bias;   // elements between groups
+    int32_t rows;          // rows of C (the offsets stay within them)
+    int32_t a_rows;        // rows of A
+    int32_t N, K, lda, ldb, ldc, ldr, ldp;
+    int32_t groups, row_div, act, gated;
+    int32_t vec;           // VEC_*: tensors that take 16-byte accesses at multiples of 8
+};
+enum { VEC_C = 1, VEC_RES = 2, VEC_PRE = 4, VEC_BIAS = 8 };
+
+__device__ __forceinline__ int clamp_row(int v, int rows) { return v < 0 ? 0 : (v > rows ? rows : v); }
+
+// Rows [lo, hi) of group g; offsets out of order or past the rows give an empty or a
+// shortened group, never an access outside the tensors.
+__device__ __forceinline__ void group_rows(const FusedArgs& p, int g, int& lo, int& hi) {
+    if (!p.offsets) {
+        lo = 0;
+        hi = p.rows;
+        return;
+    }
+    lo = clamp_row(p.offsets[g], p.rows);
+    hi = clamp_row(p.offsets[g + 1], p.rows);
+    if (hi < lo)
+        hi = lo;
+}
+
+// The A row behind row s of the product; -1 (read as zeros) where the index points
+// outside A.
+__device__ __forceinline__ int a_row_of(const FusedArgs& p, int s) {
+    if (!p.row_index)
+        return s;
+    const int v = p.row_index[s];
+    const int r = p.row_div == 1 ? v : v / p.row_div;
+    return v >= 0 && r < p.a_rows ? r : -1;
+}
+
+// The tile of workgroup `wg` when every group is cut into tiles of BM rows, each with
+// grid_n column tiles: its group, first row, end row and column tile.  False past the
+// last tile.  The order is tile_of's over all groups' row tiles, so that the row tiles of
+// one group, which share its B, run on one XCD at the same time.  Every wave computes the
+// same prefix sum over the groups, 64 at a time.
+template <int BM>
+__device__ __forceinline__ bool find_tile(const FusedArgs& p, int wg, int grid_n, int group_m, int& g,
+                                          int& row0, int& row_end, int& tn) {
+    int tm;
+    if (!p.offsets) {
+        const int gm = (p.rows + BM - 1) / BM;
+        if (wg >= gm * grid_n)
+            return false;
+        tile_of(wg, gm, grid_n, group_m, tm, tn);
+        g = 0;
+        row0 = tm * BM;
+        row_end = p.rows;
+        return true;
+    }
+    const int lane = (int)threadIdx.x & 63;
+    // all groups' tiles
+    int total = 0;
+    for (int g0 = 0; g0 < p.groups; g0 += 64) {
+        int lo = 0, hi = 0;
+        if (g0 + lane < p.groups)
+            group_rows(p, g0 + lane, lo, hi);
+        int t = (hi - lo + BM - 1) / BM;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2)
+            t += __shfl_xor(t, d);
+        total += t;
+    }
+    total = __builtin_amdgcn_readfirstlane(total);
+    if (wg >= total * grid_n)
+        return false;
+    tile_of(wg, total, grid_n, group_m, tm, tn);
+    int before = 0;
+    for (int g0 = 0; g0 < p.groups; g0 += 64) {
+        int lo = 0, hi = 0;
+        if (g0 + lane < p.groups)
+            group_rows(p, g0 + lane, lo, hi);
+        const int t = (hi - lo + BM - 1) / BM;
+        int sum = t;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int o = __shfl_up(sum, d);
+            sum += lane >= d ? o : 0;
+        }
+        const unsigned long long past = __ballot(before + sum > tm);
+        if (past) {
+            const int at = __builtin_ctzll(past);
+            g = g0 + at;
+            const int first = before + __builtin_amdgcn_readlane(sum - t, at);
+            row0 = __builtin_amdgcn_readlane(lo, at) + (tm - first) * BM;
+            row_end = __builtin_amdgcn_readlane(hi, at);
+            return true;
+        }
+        before += __builtin_amdgcn_readlane(sum, 63);
+    }
+    return false;
+}
+
+// ------------------------------------------------------------------------------------
+// Activations in fp32, with the hardware's exp2 and reciprocal (one unit in the last
+// place each): their results are rounded to 16 bits, whose half step is 2^-12 at best.
+// ------------------------------------------------------------------------------------
+__device__ __forceinline__ float logistic(float x) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * x));
+}
+
+// erfc(u) for u >= 0 as exp(-u^2) t P(t), t = 1 / (1 + 0.44 u), the form of Hastings
+// ("Approximations for Digital Computers", 1955): P, of degree 5, was fitted to
+// exp(u^2) erfc(u) t^-1 on [0, 12] for the least relative error, 5.3e-6.
+__device__ __forceinline__ float erfc_pos(float u, float& gauss) {
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.44f, u, 1.0f));
+    gauss = __builtin_amdgcn_exp2f(-1.44269504f * u * u);
+    float q = fmaf(t, -0.14623456f, 0.35104576f);
+    q = fmaf(t, q, 0.04027511f);
+    q = fmaf(t, q, 0.26383517f);
+    q = fmaf(t, q, 0.24250634f);
+    q = fmaf(t, q, 0.24856692f);
+    return t * q * gauss;
+}
+
+constexpr float kGeluTanh = 1.59576912f;    // 2 sqrt(2 / pi): (1 + tanh(u / 2)) / 2 = logistic(u)
+
+__device__ __forceinline__ float activate(int act, float x) {
+    switch (act) {
+    case ACT_RELU: return x > 0.0f ? x : (x != x ? x : 0.0f);
+    case ACT_GELU: {
+        // x Phi(x) = max(x, 0) - |x| erfc(|x| / sqrt(2)) / 2; an infinite |x| has a zero
+        // second term
+        float gauss;
+        const float a = fabsf(x);
+        const float tail = erfc_pos(0.70710678f * a, gauss);
+        return (x > 0.0f ? x : 0.0f) - (tail > 0.0f || tail != tail ? 0.5f * a * tail : 0.0f);
+    }
+    case ACT_GELU_TANH: return x * logistic(kGeluTanh * (x + 0.044715f * x * x * x));
+    case ACT_SILU: return x * logistic(x);
+    default: return x;
+    }
+}
+
+// Value and slope of an activation.
+__device__ __forceinline__ void activate_slope(int act, float x, float& value, float& slope) {
+    switch (act) {
+    case ACT_RELU:
+        value = x > 0.0f ? x : (x != x ? x : 0.0f);
+        slope = x > 0.0f ? 1.0f : 0.0f;
+        break;
+    case ACT_GELU: {
+        float gauss;                       // exp(-x^2 / 2)
+        const float a = fabsf(x);
+        const float half_tail = 0.5f * erfc_pos(0.70710678f * a, gauss);
+        const float phi = x > 0.0f ? 1.0f - half_tail : half_tail;
+        value = x * phi;
+        slope = phi + (gauss > 0.0f || gauss != gauss ? x * 0.39894228f * gauss : 0.0f);
+        break;
+    }
+    case ACT_GELU_TANH: {
+        const float p = logistic(kGeluTanh * (x + 0.044715f * x * x * x));
+        value = x * p;
+        slope = p + value * (1.0f - p) * kGeluTanh * (1.0f + 0.134145f * x * x);
+        break;
+    }
+    case ACT_SILU: {
+        const float p = logistic(x);
+        value = x * p;
+        slope = p + value * (1.0f - p);
+        break;
+    }
+    default:
+        value = x;
+        slope = 1.0f;
+    }
+}
+
+// ------------------------------------------------------------------------------------
+// Runs of eight 16-bit values: one 16-byte access where the tensor allows it and all
+// eight lie inside, else one by one.
+// ------------------------------------------------------------------------------------
+template <int DT>
+__device__ __forceinline__ float to_float(u16 h) {
+    if constexpr (DT == DT_F16)
+        return (float)__builtin_bit_cast(_Float16, h);
+    else
+        return __uint_as_float((uint32_t)h << 16);
+}
+
+template <int DT>
+__device__ __forceinline__ void unpack8(u32x4 v, float (&x)[8]) {
+    const u16x8 h = __builtin_bit_cast(u16x8, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        x[e] = to_float<DT>(h[e]);
+}
+
+template <int DT>
+__device__ __forceinline__ void load8(const u16* p, bool vec, int left, float (&x)[8]) {
+    if (vec && left >= 8) {
+        unpack8<DT>(*reinterpret_cast<const u32x4*>(p), x);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            x[e] = e < left ? to_float<DT>(p[e]) : 0.0f;
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void store8(u16* p, bool vec, int left, const float (&x)[8]) {
+    const u32x4 v{pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]), pack2<DT>(x[4], x[5]),
+                  pack2<DT>(x[6], x[7])};
+    if (vec && left >= 8) {
+        *reinterpret_cast<u32x4*>(p) = v;
+    } else {
+        const u16x8 h = __builtin_bit_cast(u16x8, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < left)
+                p[e] = h[e];
+    }
+}
+
+// The epilogue of eight columns n .. n+7 of row s (n < the width of C): z holds the
+// product there and, gated, u the product h columns on.
+template <int DT>
+__device__ __forceinline__ void emit8(const FusedArgs& p, int g, int s, int n, float (&z)[8], float (&u)[8]) {
+    const int width = p.gated ? p.N >> 1 : p.N, left = width - n;
+    if (p.bias) {
+        const u16* b = p.bias + g * p.stride_bias + n;
+        float t[8];
+        load8<DT>(b, p.vec & VEC_BIAS, left, t);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            z[e] += t[e];
+        if (p.gated) {
+            load8<DT>(b + width, p.vec & VEC_BIAS, left, t);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                u[e] += t[e];
+        }
+    }
+    if (p.preact) {
+        u16* q = p.preact + (int64_t)s * p.ldp + n;
+        store8<DT>(q, p.vec & VEC_PRE, left, z);
+        if (p.gated)
+            store8<DT>(q + width, p.vec & VEC_PRE, left, u);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        z[e] = activate(p.act, z[e]);
+        if (p.gated)
+            z[e] *= u[e];
+    }
+    if (p.residual) {
+        float t[8];
+        load8<DT>(p.residual + (int64_t)s * p.ldr + n, p.vec & VEC_RES, left, t);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            z[e] += t[e];
+    }
+    store8<DT>(p.C + (int64_t)s * p.ldc + n, p.vec & VEC_C, left, z);
+}
+
+// The B row (column of the product) of column c of column tile tn, whose tile is BN wide;
+// -1 past the end.  Gated, 32-column blocks take turns between the two halves of N, so
+// that a lane that holds a gate value also holds, one block on, the value it multiplies.
+template <int BN>
+__device__ __forceinline__ int b_row_of(const FusedArgs& p, int tn, int c) {
+    if (!p.gated) {
+        const int n = tn * BN + c;
+        return n < p.N ? n : -1;
+    }
+    const int h = p.N >> 1, n = tn * (BN / 2) + (c >> 6) * 32 + (c & 31);
+    return n < h ? n + ((c >> 5) & 1) * h : -1;
+}
+
+// ------------------------------------------------------------------------------------
+// The generic kernel: any alignment, size and layout.  64 x 64 tile, K step 16, four
+// waves of one 32 x 32 MFMA block each, masked loads of single elements into one LDS
+// stage; C through an fp32 tile in LDS.
+// ------------------------------------------------------------------------------------
+template <int DT, int LAYOUT>
+__global__ void __launch_bounds__(256) fused_generic(const FusedArgs p, int grid_n) {
+    __shared__ __attribute__((aligned(16))) u16 As[64 * 16];
+    __shared__ __attribute__((aligned(16))) u16 Bs[64 * 16];
+    __shared__ __attribute__((aligned(16))) float Cs[64 * 68];
+    int g, row0, row_end, tn;
+    if (!find_tile<64>(p, (int)blockIdx.x, grid_n, 8, g, row0, row_end, tn))
+        return;
+    const u16* B = p.B + (int64_t)g * p.stride_b;
+    const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int wm = wave >> 1, wn = wave & 1;
+    f32x16 acc = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+    // the four A rows and B rows (or, B [K,N], the one column) that this thread loads
+    int ar[4], br[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = (tid + 256 * i) >> 4;
+        ar[i] = row0 + r < row_end ? a_row_of(p, row0 + r) : -1;
+        br[i] = b_row_of<64>(p, tn, LAYOUT == LAYOUT_NK ? r : tid & 63);
+    }
+    for (int k0 = 0; k0 < p.K; k0 += 16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int e = tid + 256 * i;
+            const int gk = k0 + (e & 15);
+            As[e] = ar[i] >= 0 && gk < p.K ? p.A[(int64_t)ar[i] * p.lda + gk] : (u16)0;
+            if constexpr (LAYOUT == LAYOUT_NK) {
+                Bs[e] = br[i] >= 0 && gk < p.K ? B[(int64_t)br[i] * p.ldb + gk] : (u16)0;
+            } else {
+                const int kk = e >> 6, bk = k0 + kk;
+                Bs[(e & 63) * 16 + kk] = br[i] >= 0 && bk < p.K ? B[(int64_t)bk * p.ldb + br[i]] : (u16)0;
+            }
+        }
+        __syncthreads();
+        const u32x4 af = *reinterpret_cast<const u32x4*>(&As[(wm * 32 + (lane & 31)) * 16 + (lane >> 5) * 8]);
+        const u32x4 bf = *reinterpret_cast<const u32x4*>(&Bs[(wn * 32 + (lane & 31)) * 16 + (lane >> 5) * 8]);
+        acc = mfma_32x32x16<DT>(bf, af, acc);
+        __syncthreads();
+    }
+#pragma unroll
+    for (int v = 0; v < 16; ++v)
+        Cs[(wm * 32 + (lane & 31)) * 68 + wn * 32 + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3)] = acc[v];
+    __syncthreads();
+    const int width = p.gated ? p.N >> 1 : p.N, runs = p.gated ? 4 : 8;
+    for (int q = tid; q < 64 * runs; q += 256) {
+        const int r = q / runs, c = (q % runs) * 8;
+        const int n = tn * (runs * 8) + c;
+        if (row0 + r < row_end && n < width) {
+            float z[8], u[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                z[e] = Cs[r * 68 + c + e];
+                u[e] = p.gated ? Cs[r * 68 + c + 32 + e] : 0.0f;
+            }
+            emit8<DT>(p, g, row0 + r, n, z, u);
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------------
+// Products that sum over a group's rows (the gradient of B): for every group
+//   D_g[i,j] = sum_{s in g} left(s,i) right(s,j)
+// with left and right rows of A- and C-sized tensors, either of which may go through the
+// row index.  An empty group's D is zero.
+// ------------------------------------------------------------------------------------
+struct SumArgs {
+    const u16* left;
+    const u16* right;
+    u16* D;
+    const int32_t* offsets;
+    const int32_t* row_index;
+    int64_t stride_d;
+    int32_t rows, a_rows, groups, row_div;
+    int32_t I, J, ldl, ldr, ldd;
+    int32_t index_left, index_right;   // which of the two goes through the row index
+    int32_t vec;                       // D takes 16-byte stores at multiples of 8
+};
+
+__device__ __forceinline__ void group_rows(const SumArgs& p, int g, int& lo, int& hi) {
+    lo = p.offsets ? clamp_row(p.offsets[g], p.rows) : 0;
+    hi = p.offsets ? clamp_row(p.offsets[g + 1], p.rows) : p.rows;
+    if (hi < lo)
+        hi = lo;
+}
+
+// Row s of an operand; -1 where the index points outside it.
+__device__ __forceinline__ int sum_row(const SumArgs& p, bool indexed, int s) {
+    if (!indexed)
+        return s;
+    const int v = p.row_index[s], r = p.row_div == 1 ? v : v / p.row_div;
+    return v >= 0 && r < p.a_rows ? r : -1;
+}
+
+template <int DT>
+__global__ void __launch_bounds__(256) sum_generic(const SumArgs p, int grid_i, int grid_j) {
+    __shared__ __attribute__((aligned(16))) u16 Ls[64 * 16];
+    __shared__ __attribute__((aligned(16))) u16 Rs[64 * 16];
+    const int per = grid_i * grid_j, g = (int)blockIdx.x / per;
+    int ti, tj;
+    tile_of((int)blockIdx.x % per, grid_i, grid_j, 8, ti, tj);
+    int lo, hi;
+    group_rows(p, g, lo, hi);
+    const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int wm = wave >> 1, wn = wave & 1;
+    const int ci = ti * 64 + (tid & 63), cj = tj * 64 + (tid & 63);
+    f32x16 acc = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+    for (int s0 = lo; s0 < hi; s0 += 16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int kk = (tid >> 6) + 4 * i, s = s0 + kk;
+            u16 l = 0, r = 0;
+            if (s < hi) {
+                const int sl = sum_row(p, p.index_left, s), sr = sum_row(p, p.index_right, s);
+                if (sl >= 0 && ci < p.I)
+                    l = p.left[(int64_t)sl * p.ldl + ci];
+                if (sr >= 0 && cj < p.J)
+                    r = p.right[(int64_t)sr * p.ldr + cj];
+            }
+            Ls[(tid & 63) * 16 + kk] = l;
+            Rs[(tid & 63) * 16 + kk] = r;
+        }
+        __syncthreads();
+        const u32x4 lf = *reinterpret_cast<const u32x4*>(&Ls[(wm * 32 + (lane & 31)) * 16 + (lane >> 5) * 8]);
+        const u32x4 rf = *reinterpret_cast<const u32x4*>(&Rs[(wn * 32 + (lane & 31)) * 16 + (lane >> 5) * 8]);
+        acc = mfma_32x32x16<DT>(rf, lf, acc);
+        __syncthreads();
+    }
+    const int i = ti * 64 + wm * 32 + (lane & 31);
+    if (i < p.I) {
+        u16* row = p.D + (int64_t)g * p.stride_d + (int64_t)i * p.ldd;
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+            const int j = tj * 64 + wn * 32 + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
+            if (j < p.J)
+                row[j] = cvt1<DT>(acc[v]);
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------------
+// The epilogue's backward pass:  dZ = dC act'(Z), or gated dZ = [dC up act'(gate),
+// dC act(gate)], rounded once to the operands' type for the two products that follow, and
+// the column sums of the unrounded dZ (dbias).  One workgroup takes kSliceRows rows of a
+// group and 512 columns of dC: 64 lanes of eight columns, four rows at a time.  The column
+// sums of a slice go to a workspace row of their own and are added in slice order by
+// bias_sum, so the result does not depend on the launch order.
+// Bound by memory: 16-byte accesses, each value read and written once.
+// ------------------------------------------------------------------------------------
+constexpr int kSliceRows = 64;
+
+struct SlopeArgs {
+    const u16* dC;
+    const u16* Z;          // null: act none, not gated
+    u16* dZ;               // null: dZ is not wanted (it equals dC)
+    float* sums;           // [slices][N], or null
+    const int32_t* offsets;
+    int32_t rows, groups, N, lddc, ldz, lddz, act, gated;
+    int32_t vec;           // dC, Z, dZ all take 16-byte accesses
+};
+
+__device__ __forceinline__ void group_rows(const SlopeArgs& p, int g, int& lo, int& hi) {
+    lo = p.offsets ? clamp_row(p.offsets[g], p.rows) : 0;
+    hi = p.offsets ? clamp_row(p.offsets[g + 1], p.rows) : p.rows;
+    if (hi < lo)
+        hi = lo;
+}
+
+// Slices of kSliceRows rows of groups before group g (the workspace rows of group g start
+// there).  Called by whole waves.
+__device__ __forceinline__ int slices_before(const SlopeArgs& p, int g) {
+    int n = 0;
+    for (int i = (int)threadIdx.x & 63; i < g; i += 64) {
+        int lo, hi;
+        group_rows(p, i, lo, hi);
+        n += (hi - lo + kSliceRows - 1) / kSliceRows;
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2)
+        n += __shfl_xor(n, d);
+    return n;
+}
+
+template <int DT>
+__global__ void __launch_bounds__(256) slope_rows(const SlopeArgs p) {
+    __shared__ float red[4][2][512];
+    const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int width = p.gated ? p.N >> 1 : p.N;
+    // the slice: group, first row, end row
+    int slice = (int)blockIdx.x, lo = 0, hi = 0;
+    if (!p.offsets) {
+        lo = slice * kSliceRows;
+        hi = p.rows;
+    } else {
+        int before = 0;
+        bool found = false;
+        for (int g0 = 0; g0 < p.groups && !found; g0 += 64) {
+            int l = 0, h = 0;
+            if (g0 + lane < p.groups)
+                group_rows(p, g0 + lane, l, h);
+            const int t = (h - l + kSliceRows - 1) / kSliceRows;
+            int sum = t;
+#pragma unroll
+            for (int d = 1; d < 64; d *= 2) {
+                const int o = __shfl_up(sum, d);
+                sum += lane >= d ? o : 0;
+            }
+            const unsigned long long past = __ballot(before + sum > slice);
+            if (past) {
+                const int at = __builtin_ctzll(past);
+                const int first = before + __builtin_amdgcn_readlane(sum - t, at);
+                lo = __builtin_amdgcn_readlane(l, at) + (slice - first) * kSliceRows;
+                hi = __builtin_amdgcn_readlane(h, at);
+                found = true;
+            }
+            before += __builtin_amdgcn_readlane(sum, 63);
+        }
+        if (!found)
+            return;                       // the whole workgroup: no slice of this number
+    }
+    hi = hi < lo + kSliceRows ? hi : lo + kSliceRows;
+    const int n = ((int)blockIdx.y * 64 + lane) * 8, left = width - n;
+    float s0[8] = {0, 0, 0, 0, 0, 0, 0, 0}, s1[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (left > 0) {
+        for (int r = lo + wave; r < hi; r += 4) {
+            float dy[8], z[8], u[8];
+            load8<DT>(p.dC + (int64_t)r * p.lddc + n, p.vec, left, dy);
+            if (p.Z)
+                load8<DT>(p.Z + (int64_t)r * p.ldz + n, p.vec, left, z);
+            if (p.gated)
+                load8<DT>(p.Z + (int64_t)r * p.ldz + width + n, p.vec, left, u);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float value = 0.0f, slope = 1.0f;
+                if (p.Z)
+                    activate_slope(p.act, z[e], value, slope);
+                z[e] = dy[e] * slope;
+                if (p.gated) {
+                    z[e] *= u[e];
+                    u[e] = dy[e] * value;
+                    s1[e] += u[e];
+                }
+                s0[e] += z[e];
+            }
+            if (p.dZ) {
+                u16* q = p.dZ + (int64_t)r * p.lddz + n;
+                store8<DT>(q, p.vec, left, z);
+                if (p.gated)
+                    store8<DT>(q + width, p.vec, left, u);
+            }
+        }
+    }
+    if (!p.sums)
+        return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        red[wave][0][lane * 8 + e] = s0[e];
+        red[wave][1][lane * 8 + e] = s1[e];
+    }
+    __syncthreads();
+    for (int q = tid; q < 1024; q += 256) {
+        const int half = q >> 9, c = q & 511, col = (int)blockIdx.y * 512 + c;
+        if (col < width && (half == 0 || p.gated))
+            p.sums[(int64_t)slice * p.N + half * width + col] =
+                (red[0][half][c] + red[1][half][c]) + (red[2][half][c] + red[3][half][c]);
+    }
+}
+
+// dbias of group blockIdx.y: the slices' sums in order, four runs of slices side by side.
+static __global__ void __launch_bounds__(256) bias_sum(const SlopeArgs p, float* __restrict__ dbias) {
+    __shared__ float red[4][64];
+    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+    const int g = (int)blockIdx.y, n = (int)blockIdx.x * 64 + lane;
+    int lo, hi;
+    group_rows(p, g, lo, hi);
+    const int first = slices_before(p, g), count = (hi - lo + kSliceRows - 1) / kSliceRows;
+    const int b = first + wave * count / 4, e = first + (wave + 1) * count / 4;
+    float t = 0.0f;
+    if (n < p.N)
+        for (int i = b; i < e; ++i)
+            t += p.sums[(int64_t)i * p.N + n];
+    red[wave][lane] = t;
+    __syncthreads();
+    if (wave == 0 && n < p.N)
+        dbias[(int64_t)g * p.N + n] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+}
+
+}  // namespace tgemm

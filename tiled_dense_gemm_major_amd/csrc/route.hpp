@@ -1,0 +1,538 @@
+// gfx950 kernels of the routing of tokens to experts: the choice of k experts per token
+// with its weights, its backward pass, the plan that sorts the choices by expert, and the
+// combination of the experts' rows, forward and backward.
+#pragma once
+
+#include "fused.hpp"
+
+namespace tgemm {
+
+enum { DT_F32 = 2 };
+enum { SCORE_SOFTMAX = 0, SCORE_SIGMOID = 1 };
+enum { GROUP_MAX = 0, GROUP_TOP2 = 1 };
+
+constexpr int kMaxExperts = 1024, kMaxChoices = 64, kMaxExpertGroups = 64;
+
+template <int DT>
+__device__ __forceinline__ float load_logit(const void* p, int64_t i) {
+    if constexpr (DT == DT_F32)
+        return static_cast<const float*>(p)[i];
+    else
+        return to_float<DT>(static_cast<const u16*>(p)[i]);
+}
+
+// Orders a wave's LDS writes before its other lanes' reads: the hardware completes a
+// wave's LDS accesses in order, the compiler is kept from moving them.
+__device__ __forceinline__ void wave_lds_sync() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// Reductions over the 64 lanes of a wave, the result in every lane.
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2)
+        v = fmaxf(v, __shfl_xor(v, d));
+    return v;
+}
+__device__ __forceinline__ double wave_max(double v) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2)
+        v = fmax(v, __shfl_xor(v, d));
+    return v;
+}
+template <typename T>
+__device__ __forceinline__ T wave_sum(T v) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2)
+        v += __shfl_xor(v, d);
+    return v;
+}
+
+// ------------------------------------------------------------------------------------
+// Routing.  One wave per token; lane l holds the V experts l V .. l V + V - 1, so that the
+// lowest lane with a value holds the lowest index with it.
+//   s = softmax(x) or logistic(x), the selection value c = s + bias, or c = x where there
+//   is neither a bias nor a choice of groups (s rises with x); with groups, the experts of
+//   the topk_groups best groups only (a group's score: its largest c, or the sum of its
+//   two largest); then the k largest c, the lowest index first among equals.
+//   A logit that is -infinity or NaN, or whose c is, is never chosen; +infinity counts as
+//   the largest finite value.
+//   w = s of the chosen (the bias only selects), divided by the token's sum of them with
+//   `renormalize`, times scale.  Choices past the last candidate: id -1, weight 0.
+// SCORED: c comes from the scores, computed in fp64: in fp32 the scores of unlike logits
+// round to equal values, and which of two near experts is chosen would depend on the
+// order of a sum.  Else everything is fp32 and the choice is exact.
+// ------------------------------------------------------------------------------------
+struct RouteArgs {
+    const void* x;
+    const float* bias;
+    int32_t* ids;
+    float* weights;
+    int64_t ldx;
+    int32_t tokens, experts, k, scoring, groups, topk_groups, group_score, renormalize;
+    float scale;
+};
+
+template <int DT, int V, bool SCORED>
+__global__ void __launch_bounds__(256) route_tokens(const RouteArgs p) {
+    using T = std::conditional_t<SCORED, double, float>;
+    constexpr float kNone = -__builtin_inff();
+    __shared__ T group_c[SCORED ? 4 : 1][SCORED ? 64 * V : 1];
+    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+    const int64_t t = (int64_t)blockIdx.x * 4 + wave;
+    if (t >= p.tokens)
+        return;                            // no barrier below: a wave works on its own
+    float x[V];
+    float top = kNone;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int e = lane * V + v;
+        float a = e < p.experts ? load_logit<DT>(p.x, t * p.ldx + e) : kNone;
+        a = a == a ? a : kNone;
+        x[v] = a < __builtin_inff() ? a : 3.402823466e38f;
+        top = fmaxf(top, x[v]);
+    }
+    top = wave_max(top);
+    const float base = top > kNone ? top : 0.0f;
+    T s[V], c[V];
+    T total = 0;
+    if constexpr (SCORED) {
+        if (p.scoring == SCORE_SOFTMAX) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                s[v] = x[v] > kNone ? exp((double)x[v] - (double)base) : 0.0;
+                total += s[v];
+            }
+            total = wave_sum(total);
+            const double inv = total > 0 ? 1.0 / total : 0.0;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                s[v] *= inv;
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                s[v] = x[v] > kNone ? 1.0 / (1.0 + exp(-(double)x[v])) : 0.0;
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e = lane * V + v;
+            const double b = p.bias && e < p.experts ? (double)p.bias[e] : 0.0;
+            const double cv = s[v] + b;
+            c[v] = x[v] > kNone && cv == cv ? cv : (double)kNone;
+        }
+        if (p.groups > 1) {
+            // lane g scores group g from the token's values in LDS (a wave's LDS accesses
+            // complete in order), and the best groups are taken one at a time
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                group_c[wave][lane * V + v] = c[v];
+            wave_lds_sync();
+            const int size = p.experts / p.groups;
+            double best = kNone, second = kNone;
+            if (lane < p.groups)
+                for (int i = 0; i < size; ++i) {
+                    const double a = group_c[wave][lane * size + i];
+                    second = a > best ? best : (a > second ? a : second);
+                    best = a > best ? a : best;
+                }
+            if (p.group_score == GROUP_TOP2 && second > kNone)
+                best += second;
+            unsigned long long kept = 0;
+            for (int i = 0; i < p.topk_groups; ++i) {
+                const double m = wave_max(best);
+                if (!(m > kNone))
+                    break;
+                const int g = __builtin_ctzll(__ballot(best == m));
+                kept |= 1ull << g;
+                if (lane == g)
+                    best = kNone;
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int e = lane * V + v;
+                if (e < p.experts && !((kept >> (e / size)) & 1))
+                    c[v] = kNone;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            c[v] = x[v];
+        if (p.scoring == SCORE_SOFTMAX && !p.renormalize) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                total += x[v] > kNone ? expf(x[v] - base) : 0.0f;
+            total = wave_sum(total);
+        }
+    }
+    // the k best: the wave's largest value, its lowest lane, that lane's lowest expert
+    int id = -1;
+    T w = 0;
+    for (int i = 0; i < p.k; ++i) {
+        T m = c[0];
+#pragma unroll
+        for (int v = 1; v < V; ++v)
+            m = c[v] > m ? c[v] : m;
+        const T best = wave_max(m);
+        if (!(best > kNone))
+            break;
+        const int from = __builtin_ctzll(__ballot(m == best));
+        int at = -1;
+        T score = 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (at < 0 && c[v] == best) {
+                at = v;
+                score = SCORED ? s[v] : c[v];
+                if (lane == from)
+                    c[v] = kNone;
+            }
+        const int e = __shfl(lane * V + at, from);
+        score = __shfl(score, from);
+        if (lane == i) {
+            id = e;
+            w = score;
+        }
+    }
+    const bool chosen = id >= 0;
+    if constexpr (!SCORED) {
+        // w holds the chosen logit
+        if (p.scoring == SCORE_SIGMOID)
+            w = 1.0f / (1.0f + expf(-w));
+        else
+            w = expf(w - base) / (p.renormalize ? 1.0f : total);
+        w = chosen ? w : 0.0f;
+    }
+    if (p.renormalize) {
+        const T sum = wave_sum(w);
+        w = sum > 0 ? w / sum : w;
+    }
+    if (lane < p.k) {
+        p.ids[t * p.k + lane] = id;
+        p.weights[t * p.k + lane] = (float)(w * (T)p.scale);
+    }
+}
+
+// ------------------------------------------------------------------------------------
+// The logits' gradient for fixed choices.  With w'_j the weights before the scale and
+// g_j = scale dw_j:
+//   softmax                dx_e = s_e ([e chosen] g_e - sum_j g_j s_j)
+//   softmax, renormalized  dx_e = [e chosen] w'_e (g_e - sum_j g_j w'_j)
+//   logistic               dx_e = [e chosen] g_e s_e (1 - s_e)
+//   logistic, renormalized dx_e = [e chosen] w'_e (1 - s_e) (g_e - sum_j g_j w'_j)
+// One wave per token, everything in fp32; choices outside the experts are passed over.
+// ------------------------------------------------------------------------------------
+struct RouteGradArgs {
+    const void* x;
+    const int32_t* ids;
+    const float* dw;
+    void* dx;
+    int64_t ldx, lddx;
+    int32_t tokens, experts, k, scoring, renormalize;
+    float scale;
+};
+
+template <int DT, int V>
+__global__ void __launch_bounds__(256) route_grad(const RouteGradArgs p) {
+    constexpr float kNone = -__builtin_inff();
+    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+    const int64_t t = (int64_t)blockIdx.x * 4 + wave;
+    if (t >= p.tokens)
+        return;
+    const int my_id = lane < p.k ? p.ids[t * p.k + lane] : -1;
+    const float my_dw = lane < p.k ? p.dw[t * p.k + lane] * p.scale : 0.0f;
+    float x[V], g[V];
+    bool mine[V];
+    float top = kNone;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int e = lane * V + v;
+        float a = e < p.experts ? load_logit<DT>(p.x, t * p.ldx + e) : kNone;
+        a = a == a ? a : kNone;
+        x[v] = a < __builtin_inff() ? a : 3.402823466e38f;
+        top = fmaxf(top, x[v]);
+        g[v] = 0.0f;
+        mine[v] = false;
+    }
+    for (int i = 0; i < p.k; ++i) {
+        const int e = __builtin_amdgcn_readlane(my_id, i);
+        const float d = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(my_dw), i));
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (e == lane * V + v) {
+                mine[v] = true;
+                g[v] += d;
+            }
+    }
+    top = wave_max(top);
+    const float base = top > kNone ? top : 0.0f;
+    float s[V], total = 0.0f;               // scores; softmax: up to their common divisor
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        if (x[v] > kNone)
+            s[v] = p.scoring == SCORE_SOFTMAX ? expf(x[v] - base) : 1.0f / (1.0f + expf(-x[v]));
+        else
+            s[v] = 0.0f;
+        total += p.renormalize ? (mine[v] ? s[v] : 0.0f) : s[v];
+    }
+    const bool share = p.renormalize || p.scoring == SCORE_SOFTMAX;
+    total = wave_sum(total);
+    const float inv = share ? (total > 0.0f ? 1.0f / total : 0.0f) : 1.0f;
+    float dot = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        dot += mine[v] ? g[v] * (s[v] * inv) : 0.0f;
+    dot = share ? wave_sum(dot) : 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int e = lane * V + v;
+        if (e >= p.experts)
+            continue;
+        float d = 0.0f;
+        if (mine[v] || (p.scoring == SCORE_SOFTMAX && !p.renormalize))
+            d = s[v] * inv * (g[v] - dot);
+        if (p.scoring == SCORE_SIGMOID)
+            d *= 1.0f / (1.0f + expf(x[v]));       // 1 - s
+        if constexpr (DT == DT_F32)
+            static_cast<float*>(p.dx)[t * p.lddx + e] = d;
+        else
+            static_cast<u16*>(p.dx)[t * p.lddx + e] = cvt1<DT>(d);
+    }
+}
+
+// ------------------------------------------------------------------------------------
+// The plan: a stable counting sort of the `total` choices (token-major) by expert.
+//   offsets[e]  the first row of expert e; order[r] the choice behind row r; slots[c] the
+//   row of choice c.  A choice outside the experts has no row (slot -1); order is -1 past
+//   the last row.
+// Each wave owns a contiguous run of choices, 64 at a time, and its own count per expert
+// in LDS; lanes with equal experts find each other by one ballot per bit of the index, so
+// ranks follow the order of the choices whatever the schedule.  Up to kPlanChunk choices
+// one workgroup does all of it; beyond, plan_count writes the count of each chunk of
+// choices and plan_place, one workgroup per chunk, adds up the chunks before its own.
+// ------------------------------------------------------------------------------------
+constexpr int kPlanChunk = 4096, kPlanWaves = 16;
+
+struct PlanArgs {
+    const int32_t* ids;
+    int32_t* offsets;
+    int32_t* order;
+    int32_t* slots;
+    int32_t* counts;       // [chunks][experts] (more than one chunk)
+    int64_t total;
+    int32_t experts, chunks;
+};
+
+// The lanes of this wave whose expert is this lane's (itself included); 0 for lanes
+// without one.
+__device__ __forceinline__ unsigned long long equal_lanes(int e, int experts) {
+    const bool live = e >= 0;
+    unsigned long long m = __ballot(live);
+    for (int b = 1; b < experts; b *= 2) {
+        const unsigned long long set = __ballot(live && (e & b));
+        m &= (e & b) ? set : ~set;
+    }
+    return live ? m : 0ull;
+}
+
+__device__ __forceinline__ int plan_expert(const PlanArgs& p, int64_t i) {
+    if (i >= p.total)
+        return -1;
+    const int e = p.ids[i];
+    return e >= 0 && e < p.experts ? e : -1;
+}
+
+static __global__ void __launch_bounds__(256) plan_count(const PlanArgs p) {
+    __shared__ int count[kMaxExperts];
+    for (int e = (int)threadIdx.x; e < p.experts; e += 256)
+        count[e] = 0;
+    __syncthreads();
+    const int64_t first = (int64_t)blockIdx.x * kPlanChunk;
+    for (int i = (int)threadIdx.x; i < kPlanChunk; i += 256) {
+        const int e = plan_expert(p, first + i);
+        if (e >= 0)
+            atomicAdd(&count[e], 1);       // a sum of ones: the order does not matter
+    }
+    __syncthreads();
+    for (int e = (int)threadIdx.x; e < p.experts; e += 256)
+        p.counts[(int64_t)blockIdx.x * p.experts + e] = count[e];
+}
+
+// CAP: the most experts.
+template <int CAP>
+__global__ void __launch_bounds__(kPlanWaves * 64) plan_place(const PlanArgs p) {
+    __shared__ int waves[kPlanWaves * CAP];        // [kPlanWaves][experts]
+    __shared__ int first_row[CAP];                 // this chunk's first row of each expert
+    __shared__ int scan[kPlanWaves];
+    static_assert(CAP <= kPlanWaves * 64, "one thread per expert");
+    const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int64_t chunk0 = (int64_t)blockIdx.x * kPlanChunk;
+    const int64_t left = p.total - chunk0;
+    const int n = left < kPlanChunk ? (int)left : kPlanChunk;
+    // this wave's run of choices: whole groups of 64
+    const int per_wave = ((n + kPlanWaves * 64 - 1) / (kPlanWaves * 64)) * 64;
+    const int w0 = wave * per_wave, w1 = w0 + per_wave < n ? w0 + per_wave : n;
+    for (int i = tid; i < kPlanWaves * p.experts; i += kPlanWaves * 64)
+        waves[i] = 0;
+    __syncthreads();
+    for (int i = w0 + lane; i < w1; i += 64) {
+        const int e = plan_expert(p, chunk0 + i);
+        if (e >= 0)
+            atomicAdd(&waves[wave * p.experts + e], 1);
+    }
+    __syncthreads();
+    // each expert's choices: in all, before this chunk, and before each wave of it
+    int all = 0, before = 0;
+    if (tid < p.experts) {
+        int here = 0;
+        for (int w = 0; w < kPlanWaves; ++w) {
+            const int c = waves[w * p.experts + tid];
+            waves[w * p.experts + tid] = here;
+            here += c;
+        }
+        all = here;
+        if (p.chunks > 1) {
+            all = 0;
+            for (int b = 0; b < p.chunks; ++b) {
+                const int c = p.counts[(int64_t)b * p.experts + tid];
+                before += b < (int)blockIdx.x ? c : 0;
+                all += c;
+            }
+        }
+    }
+    // exclusive scan of `all` over the experts
+    int sum = all;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int o = __shfl_up(sum, d);
+        sum += lane >= d ? o : 0;
+    }
+    if (lane == 63)
+        scan[wave] = sum;
+    __syncthreads();
+    int base = 0, rows = 0;
+    for (int w = 0; w < kPlanWaves; ++w) {
+        base += w < wave ? scan[w] : 0;
+        rows += scan[w];
+    }
+    if (tid < p.experts) {
+        first_row[tid] = base + sum - all + before;
+        if (blockIdx.x == 0)
+            p.offsets[tid] = base + sum - all;
+    }
+    if (blockIdx.x == 0 && tid == 0)
+        p.offsets[p.experts] = rows;
+    __syncthreads();
+    // the rows, 64 choices at a time; the wave's count of an expert moves on by the lanes
+    // that hold it (a wave's LDS accesses complete in order)
+    for (int i0 = w0; i0 < w1; i0 += 64) {
+        const int i = i0 + lane;
+        const int e = i < w1 ? plan_expert(p, chunk0 + i) : -1;
+        const unsigned long long same = equal_lanes(e, p.experts);
+        int r = -1;
+        if (e >= 0) {
+            const int at = waves[wave * p.experts + e];
+            r = first_row[e] + at + __popcll(same & ((1ull << lane) - 1));
+            if (lane == 63 - __builtin_clzll(same))
+                waves[wave * p.experts + e] = at + __popcll(same);
+            p.order[r] = (int)(chunk0 + i);
+        }
+        wave_lds_sync();
+        if (i < w1)
+            p.slots[chunk0 + i] = r;
+    }
+    // no choice behind the rows past the last expert's
+    for (int i = tid; i < n; i += kPlanWaves * 64)
+        if (chunk0 + i >= rows)
+            p.order[chunk0 + i] = -1;
+}
+
+// ------------------------------------------------------------------------------------
+// The combination: Y[t] = residual[t] + sum_j w[t,j] O[slot[t,j]], summed in fp32 in the
+// order of j and rounded once.  A thread owns eight columns of a token; the k rows' loads
+// are independent of each other.  Bound by memory.
+// ------------------------------------------------------------------------------------
+struct CombineArgs {
+    const u16* O;
+    const int32_t* slots;
+    const float* weights;      // null: all one
+    const u16* residual;       // null: none; may be Y itself
+    u16* Y;
+    int32_t tokens, k, width, rows, ldo, ldr, ldy, vec;
+};
+
+template <int DT>
+__global__ void __launch_bounds__(256) combine_rows(const CombineArgs p) {
+    const int runs = (p.width + 7) / 8;
+    const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t t = q / runs;
+    if (t >= p.tokens)
+        return;
+    const int n = (int)(q - t * runs) * 8, left = p.width - n;
+    float y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (p.residual)
+        load8<DT>(p.residual + t * p.ldr + n, p.vec, left, y);
+    for (int j = 0; j < p.k; ++j) {
+        const int slot = p.slots[t * p.k + j];
+        if (slot < 0 || slot >= p.rows)
+            continue;
+        const float w = p.weights ? p.weights[t * p.k + j] : 1.0f;
+        float o[8];
+        load8<DT>(p.O + (int64_t)slot * p.ldo + n, p.vec, left, o);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            y[e] = fmaf(w, o[e], y[e]);
+    }
+    store8<DT>(p.Y + t * p.ldy + n, p.vec, left, y);
+}
+
+// Its backward pass: dO[slot[t,j]] = w[t,j] dY[t] and dw[t,j] = <dY[t], O[slot[t,j]]>, one
+// wave per choice (the waves of a token read the same dY row, from cache), the inner
+// product in fp32.  A choice without a row has dw 0.
+struct CombineGradArgs {
+    const u16* dY;
+    const u16* O;              // null: dw is not wanted
+    const int32_t* slots;
+    const float* weights;      // null: all one
+    u16* dO;                   // null: not wanted
+    float* dw;
+    int64_t choices;
+    int32_t k, width, rows, lddy, ldo, lddo, vec;
+};
+
+template <int DT>
+__global__ void __launch_bounds__(256) combine_grad(const CombineGradArgs p) {
+    const int lane = (int)threadIdx.x & 63;
+    const int64_t c = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (c >= p.choices)
+        return;
+    const int slot = p.slots[c];
+    const bool live = slot >= 0 && slot < p.rows;
+    const int64_t t = c / p.k;
+    float dot = 0.0f;
+    if (live) {
+        const float w = p.weights ? p.weights[c] : 1.0f;
+        for (int n = lane * 8; n < p.width; n += 512) {
+            const int left = p.width - n;
+            float dy[8], o[8];
+            load8<DT>(p.dY + t * p.lddy + n, p.vec, left, dy);
+            if (p.dw) {
+                load8<DT>(p.O + (int64_t)slot * p.ldo + n, p.vec, left, o);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    dot = fmaf(dy[e], o[e], dot);
+            }
+            if (p.dO) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    dy[e] *= w;
+                store8<DT>(p.dO + (int64_t)slot * p.lddo + n, p.vec, left, dy);
+            }
+        }
+    }
+    if (p.dw) {
+        dot = wave_sum(dot);
+        if (lane == 0)
+            p.dw[c] = dot;
+    }
+}
+
+}  // namespace tgemm

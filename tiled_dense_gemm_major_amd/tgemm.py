@@ -6,6 +6,8 @@ fallback: if the library is missing, every call raises.
 """
 from __future__ import annotations
 
+import collections
+import contextlib
 import ctypes
 import os
 
@@ -21,6 +23,11 @@ SPLIT_KERNELS = (KERNEL_SPLITK, KERNEL_QUAD_SPLITK)   # split K over workgroups 
 WORKSPACE_KERNELS = SPLIT_KERNELS + (KERNEL_QUAD_STREAMK,)   # need a lent workspace
 STREAMK_WORKSPACE_BYTES = 128 << 20                   # a QUAD_STREAMK configuration's
 
+F32 = 2                     # logits of moe_route and moe_route_backward only
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = range(5)
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+GROUP_MAX, GROUP_TOP2 = 0, 1
+
 SCRATCH_BYTES = 16 << 20    # the fixed per-GPU scratch of gemm_ex_noalloc
 CLOCK_STAMP_SLOTS = 4096    # compute-unit slots of one clock stamp (2 int64 each)
 
@@ -29,6 +36,9 @@ LIB_PATH = os.path.join(_PKG, "libtgemm.so")
 
 EXPORTS = ("attn_fwd_f16", "gemm_f16", "gemm_bf16", "gemm_ex", "gemm_ex_ws", "gemm_ex_noalloc",
            "gemm_strided",
+           "gemm_fused", "gemm_fused_backward", "gemm_grouped", "gemm_grouped_backward",
+           "gemm_backward_workspace_size", "moe_route", "moe_route_backward", "moe_plan",
+           "moe_plan_workspace_size", "moe_combine", "moe_combine_backward",
            "tgemm_query_config", "tgemm_query_config_ex", "tgemm_query_config_ws",
            "tgemm_workspace_size", "tgemm_list_configs", "tgemm_list_configs_ex",
            "tgemm_status_string", "tgemm_version", "tgemm_clock_stamp",
@@ -46,7 +56,12 @@ __all__ = ["F16", "BF16", "B_NK", "B_KN", "A_MK", "A_KM", "KERNEL_GENERIC", "KER
            "gemm_bf16", "gemm_ex", "gemm_ex_ws", "gemm_ex_noalloc", "gemm_strided",
            "query_config", "SCRATCH_BYTES", "CLOCK_STAMP_SLOTS",
            "query_config_packed", "query_config_ws", "workspace_size", "list_configs",
-           "attn_fwd_f16", "version", "gemm", "clock_stamp", "wall_clock_hz"]
+           "attn_fwd_f16", "version", "gemm", "clock_stamp", "wall_clock_hz",
+           "F32", "ACT_NONE", "ACT_RELU", "ACT_GELU", "ACT_GELU_TANH", "ACT_SILU",
+           "SCORE_SOFTMAX", "SCORE_SIGMOID", "GROUP_MAX", "GROUP_TOP2", "Epilogue", "Plan",
+           "gemm_fused", "gemm_fused_backward", "gemm_grouped", "gemm_grouped_backward",
+           "backward_workspace_size", "moe_route", "moe_route_backward", "moe_plan",
+           "plan_workspace_size", "moe_combine", "moe_combine_backward"]
 
 
 class TGemmError(RuntimeError):
@@ -74,6 +89,14 @@ class Config(ctypes.Structure):
         return f"Config({self.as_dict()})"
 
 
+class Epilogue(ctypes.Structure):
+    """tgemm_epilogue."""
+    _fields_ = [("activation", ctypes.c_int32), ("gated", ctypes.c_int32),
+                ("bias", ctypes.c_void_p), ("bias_stride", ctypes.c_int64),
+                ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+                ("preact", ctypes.c_void_p), ("ldp", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -96,6 +119,26 @@ def load(path: str = LIB_PATH):
     lib.attn_fwd_f16.argtypes = [i64, i64, i64, i64, vp, vp, vp, vp, i32, vp]
     lib.gemm_strided.argtypes = [i32, i64, i64, i64, vp, i64, i32, vp, i64, i32, vp, i64,
                                  cfgp, vp]
+    f32, epip, i64p = ctypes.c_float, ctypes.POINTER(Epilogue), ctypes.POINTER(ctypes.c_int64)
+    lib.gemm_fused.argtypes = [i32, i64, i64, i64, vp, i64, vp, i64, i32, vp, i64, epip, vp]
+    lib.gemm_fused_backward.argtypes = [i32, i64, i64, i64, vp, i64, vp, i64, vp, i64, i32, i32,
+                                        i32, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, i64,
+                                        vp]
+    lib.gemm_grouped.argtypes = [i32, i64, i64, i64, i64, vp, vp, i64, vp, i64, i64, vp, i64,
+                                 i64, i32, vp, i64, epip, vp]
+    lib.gemm_grouped_backward.argtypes = [i32, i64, i64, i64, i64, vp, vp, i64, vp, i64, vp,
+                                          i64, i64, vp, i64, i64, i32, i32, i32, vp, i64, vp,
+                                          i64, vp, i64, vp, i64, i64, vp, vp, i64, vp]
+    lib.gemm_backward_workspace_size.argtypes = [i64, i64, i64, i64p]
+    lib.moe_route.argtypes = [i32, i64, i64, i64, vp, i64, vp, i32, i64, i64, i32, i32, f32, vp,
+                              vp, vp]
+    lib.moe_route_backward.argtypes = [i32, i64, i64, i64, vp, i64, vp, vp, i32, i32, f32, vp,
+                                       i64, vp]
+    lib.moe_plan.argtypes = [i64, i64, vp, vp, vp, vp, vp, i64, vp]
+    lib.moe_plan_workspace_size.argtypes = [i64, i64, i64p]
+    lib.moe_combine.argtypes = [i32, i64, i64, i64, vp, i64, i64, vp, vp, vp, i64, vp, i64, vp]
+    lib.moe_combine_backward.argtypes = [i32, i64, i64, i64, vp, i64, vp, i64, i64, vp, vp, vp,
+                                         i64, vp, vp]
     lib.tgemm_query_config.argtypes = [i32, i64, i64, i64, i32, cfgp]
     lib.tgemm_query_config_ex.argtypes = [i32, i64, i64, i64, i32, i32, i32, cfgp]
     lib.tgemm_query_config_ws.argtypes = [i32, i64, i64, i64, i32, i32, cfgp,
@@ -296,3 +339,406 @@ def gemm(A, B, C=None, b_layout=B_NK, config: Config | None = None, stream=None)
     dtype = F16 if A.dtype == torch.float16 else BF16
     gemm_ex(dtype, M, N, K, A, B, C, b_layout, config, stream)
     return C
+
+
+# ---- products with an epilogue, routing and experts' products: torch tensors ---------------
+#
+# Matrices are 2-D tensors whose last dimension is contiguous; the row stride is free.  All
+# tensors of a call lie on one GPU, which need not be the current one; the work goes to the
+# given stream, or to the current stream of that GPU.  Outputs may be passed in; those that
+# are not are allocated by torch.  Nothing here is differentiable by itself: the gradients
+# are calls of their own.
+
+def _matrix(t, what, like=None, shape=None):
+    """(address, rows, columns, row stride) of a 2-D tensor, after its checks."""
+    if t.dim() != 2:
+        raise ValueError(f"{what} must have 2 dimensions, not {t.dim()}")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise TypeError(f"{what} must have the dtype and device of the operands "
+                        f"({like.dtype}, {like.device}), not {t.dtype}, {t.device}")
+    if shape is not None and (rows, cols) != shape:
+        raise ValueError(f"{what} must have shape {shape}, not {(rows, cols)}")
+    return t.data_ptr(), rows, cols, (t.stride(0) if rows > 1 else max(cols, 1))
+
+
+def _vector(t, what, like, dtype, count):
+    """The address of a contiguous tensor of `count` values of `dtype` on like's GPU."""
+    if t.dtype != dtype or t.device != like.device:
+        raise TypeError(f"{what} must be {dtype} on {like.device}, not {t.dtype} on {t.device}")
+    if t.numel() != count or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous with {count} elements, not {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+_torch_names = None
+
+
+def _torch():
+    """The torch module and what the calls below look up in it, once."""
+    global _torch_names
+    if _torch_names is None:
+        import torch
+        halves = {torch.float16: F16, torch.bfloat16: BF16}
+        _torch_names = (torch, halves, {**halves, torch.float32: F32})
+    return _torch_names
+
+
+def _operand_dtype(t, what):
+    halves = _torch()[1]
+    if t.dtype not in halves:
+        raise TypeError(f"{what} must be float16 or bfloat16, not {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be on a GPU, not on {t.device}")
+    return halves[t.dtype]
+
+
+def _on_device(t):
+    """A context with t's GPU as the current one (kernels launch on the current GPU)."""
+    torch = _torch()[0]
+    if t.device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(t.device)
+
+
+def _stream_on(t, stream):
+    if stream is None:
+        return _torch()[0].cuda.current_stream(t.device).cuda_stream
+    return stream if isinstance(stream, int) else int(stream.cuda_stream)
+
+
+def _b_sizes(B, b_layout, k):
+    """(n, k) of B's last two dimensions, with k checked against A's columns."""
+    n, kb = (B.shape[-2], B.shape[-1]) if b_layout == B_NK else (B.shape[-1], B.shape[-2])
+    if k is not None and kb != k:
+        raise ValueError(f"K mismatch: A has {k} columns, B has {kb}")
+    return n, kb
+
+
+def _epilogue(A, rows, n, width, activation, gated, bias, residual, preact, groups=None):
+    """The Epilogue of a call, or None where it adds nothing."""
+    if not activation and not gated and bias is None and residual is None and preact is None:
+        return None
+    e = Epilogue(activation=activation, gated=int(bool(gated)))
+    if bias is not None:
+        e.bias = _vector(bias, "bias", A, A.dtype, n * (groups or 1))
+        e.bias_stride = n
+    if residual is not None:
+        e.residual, _, _, e.ldr = _matrix(residual, "residual", A, (rows, width))
+    if preact is not None:
+        e.preact, _, _, e.ldp = _matrix(preact, "preact", A, (rows, n))
+    return ctypes.byref(e)
+
+
+def _width(n, gated):
+    if gated and n % 2:
+        raise ValueError(f"a gated product needs an even N, not {n}")
+    return n // 2 if gated else n
+
+
+def gemm_fused(A, B, C=None, b_layout=B_NK, bias=None, activation=ACT_NONE, gated=False,
+               residual=None, preact=None, stream=None):
+    """C = act(z) + residual with z = A x B^T (B_NK) or A x B (B_KN) + bias; gated,
+    C = act(z[:, :N/2]) * z[:, N/2:] + residual.  bias [N], residual like C (it may be C),
+    preact [M,N] takes z.  Returns C."""
+    dtype = _operand_dtype(A, "A")
+    a, m, k, lda = _matrix(A, "A")
+    b, _, _, ldb = _matrix(B, "B", A)
+    n, _ = _b_sizes(B, b_layout, k)
+    width = _width(n, gated)
+    if C is None:
+        C = A.new_empty((m, width))
+    c, _, _, ldc = _matrix(C, "C", A, (m, width))
+    e = _epilogue(A, m, n, width, activation, gated, bias, residual, preact)
+    with _on_device(A):
+        _check(load().gemm_fused(dtype, m, n, k, a, lda, b, ldb, b_layout, c, ldc, e,
+                                 _stream_on(A, stream)), "gemm_fused")
+    return C
+
+
+def backward_workspace_size(rows, n, groups=1) -> int:
+    """Workspace bytes of a backward call with dbias."""
+    nbytes = ctypes.c_int64(0)
+    _check(load().gemm_backward_workspace_size(groups, rows, n, ctypes.byref(nbytes)),
+           "gemm_backward_workspace_size")
+    return int(nbytes.value)
+
+
+def _gradient(t, like, shape, dtype=None):
+    """An output that is wanted (a tensor, or True to allocate it) or not (None, False)."""
+    if t is None or t is False:
+        return None
+    return like.new_empty(shape, dtype=dtype or like.dtype) if t is True else t
+
+
+def _gradient_buffers(A, rows, n, groups, activation, gated, preact, dZ, products, dbias,
+                      workspace):
+    """(preact address and stride, dZ address and stride, workspace address and bytes)."""
+    z = zs = d = ds = w = wb = 0
+    if activation or gated:
+        if preact is None:
+            raise ValueError("preact is needed with an activation or a gate")
+        z, _, _, zs = _matrix(preact, "preact", A, (rows, n))
+        if products:
+            if dZ is None:
+                dZ = A.new_empty((rows, n))
+            d, _, _, ds = _matrix(dZ, "dZ", A, (rows, n))
+    if dbias is not None:
+        wb = backward_workspace_size(rows, n, groups)
+        if workspace is None:
+            workspace = A.new_empty((max(wb, 16),), dtype=_torch()[0].uint8)
+        elif workspace.device != A.device or not workspace.is_contiguous():
+            raise ValueError("the workspace must be contiguous and on the operands' GPU")
+        w, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    # the tensors allocated here are kept until the call has been enqueued
+    return z, zs, d, ds, w, wb, (dZ, workspace)
+
+
+def gemm_fused_backward(dC, A, B, preact=None, b_layout=B_NK, activation=ACT_NONE, gated=False,
+                        dZ=None, dA=True, dB=True, dbias=False, workspace=None, stream=None):
+    """(dA, dB, dbias) of gemm_fused for dC.  dA, dB, dbias: True (allocated), a tensor to
+    fill, or None / False (not wanted; returned as None).  preact [M,N] is what the forward
+    call kept (unused without an activation and a gate); dZ [M,N] takes the gradient of z
+    (allocated if None; may be preact).  dbias is fp32 [N]."""
+    dtype = _operand_dtype(A, "A")
+    torch = _torch()[0]
+    a, m, k, lda = _matrix(A, "A")
+    b, b_rows, b_cols, ldb = _matrix(B, "B", A)
+    n, _ = _b_sizes(B, b_layout, k)
+    dc, _, _, lddc = _matrix(dC, "dC", A, (m, _width(n, gated)))
+    dA, dB = _gradient(dA, A, (m, k)), _gradient(dB, A, (b_rows, b_cols))
+    dbias = _gradient(dbias, A, (n,), torch.float32)
+    da, _, _, ldda = (0, 0, 0, 0) if dA is None else _matrix(dA, "dA", A, (m, k))
+    db, _, _, lddb = (0, 0, 0, 0) if dB is None else _matrix(dB, "dB", A, (b_rows, b_cols))
+    dbv = 0 if dbias is None else _vector(dbias, "dbias", A, torch.float32, n)
+    z, ldz, d, lddz, w, wb, keep = _gradient_buffers(
+        A, m, n, 1, activation, gated, preact, dZ, dA is not None or dB is not None, dbias,
+        workspace)
+    with _on_device(A):
+        _check(load().gemm_fused_backward(dtype, m, n, k, dc, lddc, a, lda, b, ldb, b_layout,
+                                          activation, int(bool(gated)), z, ldz, d, lddz, da,
+                                          ldda, db, lddb, dbv, w, wb, _stream_on(A, stream)),
+               "gemm_fused_backward")
+    return dA, dB, dbias
+
+
+def _stack(B, what, like, shape=None):
+    """(address, row stride, group stride) of a 3-D tensor [groups, rows, columns]."""
+    if B.dim() != 3:
+        raise ValueError(f"{what} must have 3 dimensions, not {B.dim()}")
+    if shape is not None and tuple(B.shape) != shape:
+        raise ValueError(f"{what} must have shape {shape}, not {tuple(B.shape)}")
+    if B.dtype != like.dtype or B.device != like.device:
+        raise TypeError(f"{what} must have the dtype and device of the operands "
+                        f"({like.dtype}, {like.device}), not {B.dtype}, {B.device}")
+    groups, rows, cols = B.shape
+    if cols > 1 and B.stride(2) != 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    return (B.data_ptr(), B.stride(1) if rows > 1 else max(cols, 1),
+            B.stride(0) if groups > 1 else 0)
+
+
+def _groups(A, B, offsets, row_index, row_div):
+    """(rows, offsets address, row index address) of a grouped call."""
+    torch = _torch()[0]
+    off = _vector(offsets, "offsets", A, torch.int32, B.shape[0] + 1)
+    if row_index is None:
+        return A.shape[0], off, 0
+    return row_index.numel(), off, _vector(row_index, "row_index", A, torch.int32,
+                                           row_index.numel())
+
+
+def gemm_grouped(A, B, offsets, C=None, row_index=None, row_div=1, b_layout=B_NK, bias=None,
+                 activation=ACT_NONE, gated=False, residual=None, preact=None, stream=None):
+    """One product per group of rows, with the epilogue of gemm_fused: rows
+    offsets[g] .. offsets[g+1]-1 of C take B[g] (and bias[g]).  B is [groups, N, K] (B_NK) or
+    [groups, K, N] (B_KN); with row_index, row s of C reads row row_index[s] // row_div of A.
+    Rows of C and preact outside every group keep what they held.  Returns C."""
+    dtype = _operand_dtype(A, "A")
+    a, a_rows, k, lda = _matrix(A, "A")
+    b, ldb, stride_b = _stack(B, "B", A)
+    n, _ = _b_sizes(B, b_layout, k)
+    width, groups = _width(n, gated), B.shape[0]
+    rows, off, idx = _groups(A, B, offsets, row_index, row_div)
+    if C is None:
+        C = A.new_empty((rows, width))
+    c, _, _, ldc = _matrix(C, "C", A, (rows, width))
+    e = _epilogue(A, rows, n, width, activation, gated, bias, residual, preact, groups)
+    with _on_device(A):
+        _check(load().gemm_grouped(dtype, groups, rows, n, k, off, idx, row_div, a, a_rows, lda,
+                                   b, ldb, stride_b, b_layout, c, ldc, e,
+                                   _stream_on(A, stream)), "gemm_grouped")
+    return C
+
+
+def gemm_grouped_backward(dC, A, B, offsets, preact=None, row_index=None, row_div=1,
+                          b_layout=B_NK, activation=ACT_NONE, gated=False, dZ=None, dA=True,
+                          dB=True, dbias=False, workspace=None, stream=None):
+    """(dA, dB, dbias) of gemm_grouped for dC: dA one row per row of C, dB like B, dbias fp32
+    [groups, N].  Outputs and the other arguments as in gemm_fused_backward."""
+    dtype = _operand_dtype(A, "A")
+    torch = _torch()[0]
+    a, a_rows, k, lda = _matrix(A, "A")
+    b, ldb, stride_b = _stack(B, "B", A)
+    n, _ = _b_sizes(B, b_layout, k)
+    groups, b_shape = B.shape[0], tuple(B.shape)
+    rows, off, idx = _groups(A, B, offsets, row_index, row_div)
+    dc, _, _, lddc = _matrix(dC, "dC", A, (rows, _width(n, gated)))
+    dA, dB = _gradient(dA, A, (rows, k)), _gradient(dB, A, b_shape)
+    dbias = _gradient(dbias, A, (groups, n), torch.float32)
+    da, _, _, ldda = (0, 0, 0, 0) if dA is None else _matrix(dA, "dA", A, (rows, k))
+    db, lddb, stride_db = (0, 0, 0) if dB is None else _stack(dB, "dB", A, b_shape)
+    dbv = 0 if dbias is None else _vector(dbias, "dbias", A, torch.float32, groups * n)
+    z, ldz, d, lddz, w, wb, keep = _gradient_buffers(
+        A, rows, n, groups, activation, gated, preact, dZ, dA is not None or dB is not None,
+        dbias, workspace)
+    with _on_device(A):
+        _check(load().gemm_grouped_backward(
+            dtype, groups, rows, n, k, off, idx, row_div, dc, lddc, a, a_rows, lda, b, ldb,
+            stride_b, b_layout, activation, int(bool(gated)), z, ldz, d, lddz, da, ldda, db,
+            lddb, stride_db, dbv, w, wb, _stream_on(A, stream)), "gemm_grouped_backward")
+    return dA, dB, dbias
+
+
+def _logits(x, what="logits"):
+    names = _torch()[2]
+    if x.dtype not in names:
+        raise TypeError(f"{what} must be float16, bfloat16 or float32, not {x.dtype}")
+    if not x.is_cuda:
+        raise ValueError(f"{what} must be on a GPU, not on {x.device}")
+    return (names[x.dtype], *_matrix(x, what))
+
+
+def moe_route(logits, k, scoring=SCORE_SOFTMAX, bias=None, groups=1, topk_groups=None,
+              group_score=GROUP_MAX, renormalize=True, scale=1.0, ids=None, weights=None,
+              stream=None):
+    """(ids, weights) [tokens, k] of the k experts of each token, from logits
+    [tokens, experts]: int32 and fp32, in descending order of the selection values.  bias is
+    fp32 [experts] and only selects; groups and topk_groups limit the choice to the best
+    groups of experts.  Masked logits (-inf, NaN) are never chosen: id -1, weight 0."""
+    torch = _torch()[0]
+    dtype, x, tokens, experts, ldx = _logits(logits)
+    if ids is None:
+        ids = logits.new_empty((tokens, k), dtype=torch.int32)
+    if weights is None:
+        weights = logits.new_empty((tokens, k), dtype=torch.float32)
+    i = _vector(ids, "ids", logits, torch.int32, tokens * k)
+    w = _vector(weights, "weights", logits, torch.float32, tokens * k)
+    bv = 0 if bias is None else _vector(bias, "bias", logits, torch.float32, experts)
+    with _on_device(logits):
+        _check(load().moe_route(dtype, tokens, experts, k, x, ldx, bv, scoring, groups,
+                                groups if topk_groups is None else topk_groups, group_score,
+                                int(bool(renormalize)), scale, i, w,
+                                _stream_on(logits, stream)), "moe_route")
+    return ids, weights
+
+
+def moe_route_backward(logits, ids, dweights, scoring=SCORE_SOFTMAX, renormalize=True,
+                       scale=1.0, dlogits=None, stream=None):
+    """The logits' gradient [tokens, experts] from the weights' gradient [tokens, k] fp32, for
+    the choices that moe_route made."""
+    torch = _torch()[0]
+    dtype, x, tokens, experts, ldx = _logits(logits)
+    k = ids.shape[-1]
+    i = _vector(ids, "ids", logits, torch.int32, tokens * k)
+    dw = _vector(dweights, "dweights", logits, torch.float32, tokens * k)
+    if dlogits is None:
+        dlogits = logits.new_empty((tokens, experts))
+    dx, _, _, lddx = _matrix(dlogits, "dlogits", logits, (tokens, experts))
+    with _on_device(logits):
+        _check(load().moe_route_backward(dtype, tokens, experts, k, x, ldx, i, dw, scoring,
+                                         int(bool(renormalize)), scale, dx, lddx,
+                                         _stream_on(logits, stream)), "moe_route_backward")
+    return dlogits
+
+
+Plan = collections.namedtuple("Plan", "offsets order slots")
+
+
+def plan_workspace_size(choices, experts) -> int:
+    """Workspace bytes of moe_plan (0 up to 4096 choices)."""
+    nbytes = ctypes.c_int64(0)
+    _check(load().moe_plan_workspace_size(choices, experts, ctypes.byref(nbytes)),
+           "moe_plan_workspace_size")
+    return int(nbytes.value)
+
+
+def moe_plan(ids, experts, offsets=None, order=None, slots=None, workspace=None, stream=None):
+    """The choices ids (int32, [tokens, k]) sorted by expert, as Plan(offsets [experts + 1],
+    order [tokens * k], slots like ids): the offsets of gemm_grouped, its row_index (with
+    row_div = k) and the slots of moe_combine."""
+    torch = _torch()[0]
+    if not ids.is_cuda:
+        raise ValueError(f"ids must be on a GPU, not on {ids.device}")
+    count = ids.numel()
+    i = _vector(ids, "ids", ids, torch.int32, count)
+    if offsets is None:
+        offsets = ids.new_empty((experts + 1,))
+    if order is None:
+        order = ids.new_empty((count,))
+    if slots is None:
+        slots = ids.new_empty(ids.shape)
+    need = plan_workspace_size(count, experts)
+    if workspace is None and need:
+        workspace = ids.new_empty((need // 4,))
+    w = wb = 0
+    if workspace is not None:
+        if workspace.device != ids.device or not workspace.is_contiguous():
+            raise ValueError("the workspace must be contiguous and on the ids' GPU")
+        w, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    off = _vector(offsets, "offsets", ids, torch.int32, experts + 1)
+    o = _vector(order, "order", ids, torch.int32, count)
+    s = _vector(slots, "slots", ids, torch.int32, count)
+    with _on_device(ids):
+        _check(load().moe_plan(count, experts, i, off, o, s, w, wb, _stream_on(ids, stream)),
+               "moe_plan")
+    return Plan(offsets, order, slots)
+
+
+def moe_combine(O, slots, weights=None, residual=None, Y=None, stream=None):
+    """Y[t] = residual[t] + sum_j weights[t,j] O[slots[t,j]], slots int32 [tokens, k] (one
+    outside O adds nothing), weights fp32 [tokens, k] or None (all one).  residual may be Y.
+    Returns Y."""
+    torch = _torch()[0]
+    dtype = _operand_dtype(O, "O")
+    o, rows, width, ldo = _matrix(O, "O")
+    if slots.dim() != 2:
+        raise ValueError("slots must be [tokens, k]")
+    tokens, k = slots.shape
+    s = _vector(slots, "slots", O, torch.int32, tokens * k)
+    w = 0 if weights is None else _vector(weights, "weights", O, torch.float32, tokens * k)
+    if Y is None:
+        Y = O.new_empty((tokens, width))
+    y, _, _, ldy = _matrix(Y, "Y", O, (tokens, width))
+    r, _, _, ldr = (0, 0, 0, 0) if residual is None else _matrix(residual, "residual", O,
+                                                                (tokens, width))
+    with _on_device(O):
+        _check(load().moe_combine(dtype, tokens, k, width, o, rows, ldo, s, w, r, ldr, y, ldy,
+                                  _stream_on(O, stream)), "moe_combine")
+    return Y
+
+
+def moe_combine_backward(dY, O, slots, weights=None, dO=True, dweights=True, stream=None):
+    """(dO, dweights) of moe_combine: dO[slots[t,j]] = weights[t,j] dY[t] (rows that no slot
+    names keep what they held), dweights[t,j] = <dY[t], O[slots[t,j]]> in fp32.  Either:
+    True (allocated), a tensor to fill, or None / False (not wanted)."""
+    torch = _torch()[0]
+    dtype = _operand_dtype(O, "O")
+    o, rows, width, ldo = _matrix(O, "O")
+    if slots.dim() != 2:
+        raise ValueError("slots must be [tokens, k]")
+    tokens, k = slots.shape
+    dy, _, _, lddy = _matrix(dY, "dY", O, (tokens, width))
+    s = _vector(slots, "slots", O, torch.int32, tokens * k)
+    w = 0 if weights is None else _vector(weights, "weights", O, torch.float32, tokens * k)
+    dO = _gradient(dO, O, (rows, width))
+    dweights = _gradient(dweights, O, (tokens, k), torch.float32)
+    do, _, _, lddo = (0, 0, 0, 0) if dO is None else _matrix(dO, "dO", O, (rows, width))
+    dw = 0 if dweights is None else _vector(dweights, "dweights", O, torch.float32, tokens * k)
+    with _on_device(O):
+        _check(load().moe_combine_backward(dtype, tokens, k, width, dy, lddy, o, rows, ldo, s, w,
+                                           do, lddo, dw, _stream_on(O, stream)),
+               "moe_combine_backward")
+    return dO, dweights
