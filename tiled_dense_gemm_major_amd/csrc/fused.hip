@@ -8,6 +8,29 @@
 
 #include "fused_launch.hpp"
 
+namespace tgemm {
+
+// dbias of group blockIdx.y: the slices' sums in order, four runs of slices side by side.
+__global__ void __launch_bounds__(256) bias_sum(const SlopeArgs p, float* __restrict__ dbias) {
+    __shared__ float red[4][64];
+    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+    const int g = (int)blockIdx.y, n = (int)blockIdx.x * 64 + lane;
+    int lo, hi;
+    group_rows(p, g, lo, hi);
+    const int first = slices_before(p, g), count = (hi - lo + kSliceRows - 1) / kSliceRows;
+    const int b = first + wave * count / 4, e = first + (wave + 1) * count / 4;
+    float t = 0.0f;
+    if (n < p.N)
+        for (int i = b; i < e; ++i)
+            t += p.sums[(int64_t)i * p.N + n];
+    red[wave][lane] = t;
+    __syncthreads();
+    if (wave == 0 && n < p.N)
+        dbias[(int64_t)g * p.N + n] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+}
+
+}  // namespace tgemm
+
 namespace {
 
 using tgemm::u16;
@@ -102,8 +125,50 @@ int64_t most_tiles(const Layer& l, int64_t bm) {
     return l.rows / bm + (l.groups < l.rows ? l.groups : l.rows);
 }
 
+// The tiled kernels move 16-byte pieces of A and B through buffers whose offsets stay below
+// 2^31 bytes: one group's B, the rows of an A tile, or all of A through a row index.
+constexpr int64_t kMaxBufferBytes = int64_t(1) << 31;
+
+bool tiles_fit(const Layer& l) {
+    const bool kn = l.b_layout == TGEMM_B_KN;
+    return al16(l.A) && al16(l.B) && l.lda % 8 == 0 && l.ldb % 8 == 0 && (l.groups == 1 || l.stride_b % 8 == 0) &&
+           l.k % 8 == 0 && (!kn || l.width() % 8 == 0) && l.lda <= (int64_t(1) << 21) &&
+           2 * span(l.b_rows(), l.b_cols(), l.ldb) <= kMaxBufferBytes &&
+           (!l.row_index || 2 * span(l.a_rows, l.k, l.lda) <= kMaxBufferBytes);
+}
+
+// The tile form of a product over rows: the least of (waves of workgroups on 256 compute
+// units) x (one tile's time relative to 256x256), the groups taken as equal.
+tgemm_fused::Form choose_rows(const Layer& l) {
+    static const double kTime[tgemm_fused::FORMS] = {1.0, 0.36, 0.22};
+    static const int kPerUnit[tgemm_fused::FORMS] = {1, 2, 2};
+    int best = 0;
+    double least = 0;
+    for (int f = 0; f < tgemm_fused::FORMS; ++f) {
+        const int64_t live = l.offsets ? (l.groups < l.rows ? l.groups : l.rows) : 1;
+        const int64_t tiles = live * cdiv(cdiv(l.rows, live), tgemm_fused::kTiles[f].m) *
+                              cdiv(l.width(), tgemm_fused::kTiles[f].n / (l.gated ? 2 : 1));
+        const double cost = (double)cdiv(tiles, 256 * kPerUnit[f]) * kPerUnit[f] * kTime[f];
+        if (f == 0 || cost < least) {
+            best = f;
+            least = cost;
+        }
+    }
+    return (tgemm_fused::Form)best;
+}
+
 // The product over rows of groups, with its epilogue.
 int launch_rows(const Layer& l, const FusedArgs& p, hipStream_t s) {
+    if (tiles_fit(l)) {
+        const tgemm_fused::Form form = choose_rows(l);
+        const int64_t tm = most_tiles(l, tgemm_fused::kTiles[form].m);
+        const int64_t tn = cdiv(l.width(), tgemm_fused::kTiles[form].n / (l.gated ? 2 : 1));
+        if (tm * tn > kMaxDim)
+            return TGEMM_ERR_UNSUPPORTED;
+        (void)hipGetLastError();
+        return status(l.b_layout == TGEMM_B_NK ? tgemm_fused::rows_tiled_nk(l.dtype, form, p, tm, (int)tn, s)
+                                               : tgemm_fused::rows_tiled_kn(l.dtype, form, p, tm, (int)tn, s));
+    }
     const int64_t grid_n = l.gated ? cdiv(l.n / 2, 32) : cdiv(l.n, 64);
     const int64_t grid = most_tiles(l, 64) * grid_n;
     if (grid > kMaxDim)
@@ -216,6 +281,18 @@ struct Gradients {
 };
 
 int launch_sum(const Layer& l, const SumArgs& p, hipStream_t s) {
+    const auto through = [&](bool indexed, int64_t cols, int64_t ld) {
+        return ld <= (int64_t(1) << 23) && cols % 8 == 0 && ld % 8 == 0 &&
+               (!indexed || 2 * span(p.a_rows, cols, ld) <= kMaxBufferBytes);
+    };
+    if (al16(p.left) && al16(p.right) && through(p.index_left, p.I, p.ldl) && through(p.index_right, p.J, p.ldr)) {
+        const int64_t t256 = l.groups * cdiv(p.I, 256) * cdiv(p.J, 256);
+        if (l.groups * cdiv(p.I, 128) * cdiv(p.J, 128) > kMaxDim)
+            return TGEMM_ERR_UNSUPPORTED;
+        tgemm_fused::Form f = t256 >= 128 ? tgemm_fused::FORM_256 : tgemm_fused::FORM_128;
+        (void)hipGetLastError();
+        return status(tgemm_fused::sum_tiled(l.dtype, f, p, s));
+    }
     const int64_t gi = cdiv(p.I, 64), gj = cdiv(p.J, 64);
     if (l.groups * gi * gj > kMaxDim)
         return TGEMM_ERR_UNSUPPORTED;

@@ -148,6 +148,21 @@ __device__ __forceinline__ float erfc_pos(float u, float& gauss) {
     return t * q * gauss;
 }
 
+// The same with P of degree 7 and t = 1 / (1 + 0.43 u), 1.8e-7: for the slopes, whose
+// column sums are kept in fp32.
+__device__ __forceinline__ float erfc_pos_fine(float u, float& gauss) {
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.43f, u, 1.0f));
+    gauss = __builtin_amdgcn_exp2f(-1.44269504f * u * u);
+    float q = fmaf(t, 0.07092017f, -0.29907167f);
+    q = fmaf(t, q, 0.3647995f);
+    q = fmaf(t, q, -0.06887345f);
+    q = fmaf(t, q, 0.23823461f);
+    q = fmaf(t, q, 0.20746253f);
+    q = fmaf(t, q, 0.24398948f);
+    q = fmaf(t, q, 0.24253866f);
+    return t * q * gauss;
+}
+
 constexpr float kGeluTanh = 1.59576912f;    // 2 sqrt(2 / pi): (1 + tanh(u / 2)) / 2 = logistic(u)
 
 __device__ __forceinline__ float activate(int act, float x) {
@@ -177,7 +192,7 @@ __device__ __forceinline__ void activate_slope(int act, float x, float& value, f
     case ACT_GELU: {
         float gauss;                       // exp(-x^2 / 2)
         const float a = fabsf(x);
-        const float half_tail = 0.5f * erfc_pos(0.70710678f * a, gauss);
+        const float half_tail = 0.5f * erfc_pos_fine(0.70710678f * a, gauss);
         const float phi = x > 0.0f ? 1.0f - half_tail : half_tail;
         value = x * phi;
         slope = phi + (gauss > 0.0f || gauss != gauss ? x * 0.39894228f * gauss : 0.0f);
@@ -247,24 +262,34 @@ __device__ __forceinline__ void store8(u16* p, bool vec, int left, const float (
     }
 }
 
-// The epilogue of eight columns n .. n+7 of row s (n < the width of C): z holds the
-// product there and, gated, u the product h columns on.
+// The bias of eight columns n .. n+7 of group g (and, gated, of the eight h on).
 template <int DT>
-__device__ __forceinline__ void emit8(const FusedArgs& p, int g, int s, int n, float (&z)[8], float (&u)[8]) {
-    const int width = p.gated ? p.N >> 1 : p.N, left = width - n;
-    if (p.bias) {
+__device__ __forceinline__ void load_bias(const FusedArgs& p, int g, int n, int width, float (&bz)[8],
+                                          float (&bu)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        bz[e] = bu[e] = 0.0f;
+    if (p.bias && n < width) {
         const u16* b = p.bias + g * p.stride_bias + n;
-        float t[8];
-        load8<DT>(b, p.vec & VEC_BIAS, left, t);
+        load8<DT>(b, p.vec & VEC_BIAS, width - n, bz);
+        if (p.gated)
+            load8<DT>(b + width, p.vec & VEC_BIAS, width - n, bu);
+    }
+}
+
+// The epilogue of eight columns n .. n+7 of row s (n < width, C's): z holds the product
+// there and, gated, u the product h columns on; bz and bu their bias, r the residual.
+template <int DT>
+__device__ __forceinline__ void finish8(const FusedArgs& p, int s, int n, int width, float (&z)[8], float (&u)[8],
+                                        const float (&bz)[8], const float (&bu)[8], const float (&r)[8]) {
+    const int left = width - n;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        z[e] += bz[e];
+    if (p.gated) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            z[e] += t[e];
-        if (p.gated) {
-            load8<DT>(b + width, p.vec & VEC_BIAS, left, t);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                u[e] += t[e];
-        }
+            u[e] += bu[e];
     }
     if (p.preact) {
         u16* q = p.preact + (int64_t)s * p.ldp + n;
@@ -272,20 +297,46 @@ __device__ __forceinline__ void emit8(const FusedArgs& p, int g, int s, int n, f
         if (p.gated)
             store8<DT>(q + width, p.vec & VEC_PRE, left, u);
     }
+    // one uniform branch per run of eight
+    switch (p.act) {
+    case ACT_RELU:
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        z[e] = activate(p.act, z[e]);
-        if (p.gated)
+        for (int e = 0; e < 8; ++e)
+            z[e] = activate(ACT_RELU, z[e]);
+        break;
+    case ACT_GELU:
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            z[e] = activate(ACT_GELU, z[e]);
+        break;
+    case ACT_GELU_TANH:
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            z[e] = activate(ACT_GELU_TANH, z[e]);
+        break;
+    case ACT_SILU:
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            z[e] = activate(ACT_SILU, z[e]);
+        break;
+    default: break;
+    }
+    if (p.gated) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
             z[e] *= u[e];
     }
     if (p.residual) {
-        float t[8];
-        load8<DT>(p.residual + (int64_t)s * p.ldr + n, p.vec & VEC_RES, left, t);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            z[e] += t[e];
+            z[e] += r[e];
     }
     store8<DT>(p.C + (int64_t)s * p.ldc + n, p.vec & VEC_C, left, z);
+}
+
+template <int DT>
+__device__ __forceinline__ void load_residual(const FusedArgs& p, int s, int n, int width, float (&r)[8]) {
+    load8<DT>(p.residual + (int64_t)s * p.ldr + n, p.vec & VEC_RES, width - n, r);
 }
 
 // The B row (column of the product) of column c of column tile tn, whose tile is BN wide;
@@ -360,7 +411,11 @@ __global__ void __launch_bounds__(256) fused_generic(const FusedArgs p, int grid
                 z[e] = Cs[r * 68 + c + e];
                 u[e] = p.gated ? Cs[r * 68 + c + 32 + e] : 0.0f;
             }
-            emit8<DT>(p, g, row0 + r, n, z, u);
+            float bz[8], bu[8], res[8] = {};
+            load_bias<DT>(p, g, n, width, bz, bu);
+            if (p.residual)
+                load_residual<DT>(p, row0 + r, n, width, res);
+            finish8<DT>(p, row0 + r, n, width, z, u, bz, bu, res);
         }
     }
 }
@@ -571,25 +626,6 @@ __global__ void __launch_bounds__(256) slope_rows(const SlopeArgs p) {
             p.sums[(int64_t)slice * p.N + half * width + col] =
                 (red[0][half][c] + red[1][half][c]) + (red[2][half][c] + red[3][half][c]);
     }
-}
-
-// dbias of group blockIdx.y: the slices' sums in order, four runs of slices side by side.
-static __global__ void __launch_bounds__(256) bias_sum(const SlopeArgs p, float* __restrict__ dbias) {
-    __shared__ float red[4][64];
-    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
-    const int g = (int)blockIdx.y, n = (int)blockIdx.x * 64 + lane;
-    int lo, hi;
-    group_rows(p, g, lo, hi);
-    const int first = slices_before(p, g), count = (hi - lo + kSliceRows - 1) / kSliceRows;
-    const int b = first + wave * count / 4, e = first + (wave + 1) * count / 4;
-    float t = 0.0f;
-    if (n < p.N)
-        for (int i = b; i < e; ++i)
-            t += p.sums[(int64_t)i * p.N + n];
-    red[wave][lane] = t;
-    __syncthreads();
-    if (wave == 0 && n < p.N)
-        dbias[(int64_t)g * p.N + n] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
 }
 
 }  // namespace tgemm

@@ -1,0 +1,30 @@
+// libtgemm: the tiled kernels that sum over a group's rows.
+#include "fused_launch.hpp"
+#include "fused_tile.hpp"
+
+namespace tgemm_fused {
+
+hipError_t sum_tiled(int dtype, Form form, const SumArgs& p, hipStream_t s) {
+#define SUM(DT, BI, BJ, WI, WJ, ST, OCC)                                                   \
+    do {                                                                                   \
+        const int gi = (p.I + BI - 1) / BI, gj = (p.J + BJ - 1) / BJ;                      \
+        hipLaunchKernelGGL((tgemm::sum_tiled<DT, BI, BJ, WI, WJ, ST, OCC>),                \
+                           dim3((unsigned)((int64_t)p.groups * gi * gj)), dim3(WI * WJ * 64), 0, s, p, gi, gj); \
+    } while (0)
+#define FORM(BI, BJ, WI, WJ, ST, OCC)                                                      \
+    do {                                                                                   \
+        if (dtype == tgemm::DT_F16)                                                        \
+            SUM(0, BI, BJ, WI, WJ, ST, OCC);                                               \
+        else                                                                               \
+            SUM(1, BI, BJ, WI, WJ, ST, OCC);                                               \
+    } while (0)
+    if (form == FORM_256)
+        FORM(256, 256, 2, 4, 2, 2);
+    else
+        FORM(128, 128, 2, 2, 2, 2);
+#undef FORM
+#undef SUM
+    return hipGetLastError();
+}
+
+}  // namespace tgemm_fused

@@ -1,0 +1,438 @@
+// The tiled kernels of the fused and grouped products for aligned operands: MFMA tiles fed
+// by direct-to-LDS loads.
+#pragma once
+
+#include "fused.hpp"
+
+namespace tgemm {
+
+// Keeps the compiler from moving a wave's LDS reads above its LDS writes of other lanes'
+// values; the hardware completes a wave's LDS accesses in order.
+__device__ __forceinline__ void wave_lds_order() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// ------------------------------------------------------------------------------------
+// Operand tiles of 64 k, staged by 1 KiB direct-to-LDS loads (64 lanes x 16 bytes, lane l
+// landing at byte 16 l), LD loads per wave.
+//   KRows: R rows of 64 k (128 bytes each, 8 rows per load).  Chunk c of row r sits at
+//     c ^ swz(r): the row-wise operand reads of 32 lanes are free of bank conflicts.
+//   KCols: 64 k rows of R columns (2 R bytes each, 512 / R rows per load), read by the
+//     transposing LDS read: four k rows of 16 columns per 16 lanes, so that lanes 0-31 read
+//     4 rows x 64 bytes.  The rows are a whole number of 256-byte bank windows apart (R >=
+//     128; half of one, R = 64), so chunk c of row k sits at c ^ kc_swz(k), which puts the
+//     four pieces into four different quarters of the window.
+// Offsets are bytes below 2^31; a lane whose row, column or k lies outside reads at
+// kOutOfRange, which the buffer's range check turns into zeros.
+// ------------------------------------------------------------------------------------
+constexpr int kTileK = 64;
+
+template <int R, int NW>
+struct KRows {
+    static constexpr int LD = R / 8 / NW;
+    static_assert(LD >= 2 && LD % 2 == 0, "whole load pairs per wave");
+    uint32_t off[LD];
+    int kc[2];                               // this lane's k in a load (by the load's parity)
+    // byte_of(r): the byte offset of tile row r, or kOutOfRange
+    template <typename F>
+    __device__ __forceinline__ void init(int wave, int lane, F&& byte_of) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            kc[q] = ((lane & 7) ^ swz<8>(8 * q + (lane >> 3))) * 8;
+#pragma unroll
+        for (int i = 0; i < LD; ++i) {
+            const uint32_t o = byte_of(8 * (wave * LD + i) + (lane >> 3));
+            off[i] = o == kOutOfRange ? o : o + (uint32_t)kc[i & 1] * 2u;
+        }
+    }
+    __device__ __forceinline__ void load(rsrc4_t r, uint32_t lds, int wave, int k0, int K) const {
+        const uint32_t v0 = k0 + kc[0] < K ? 0u : kOutOfRange, v1 = k0 + kc[1] < K ? 0u : kOutOfRange;
+#pragma unroll
+        for (int i = 0; i < LD; ++i)
+            dma16_at(r, lds + (uint32_t)((wave * LD + i) * 1024), off[i] | (i & 1 ? v1 : v0), (uint32_t)k0 * 2u);
+    }
+};
+
+template <int R>
+__device__ __forceinline__ int kc_swz(int k) {
+    return R >= 128 ? 4 * (k & 3) : 4 * ((k >> 1) & 1);
+}
+
+template <int R, int NW>
+struct KCols {
+    static constexpr int LD = R / 8 / NW, CH = R / 8, KPL = 64 / CH;
+    static_assert(R == 64 || R == 128 || R == 256, "tile columns");
+    static_assert(LD >= 1, "whole loads per wave");
+    // the k row of this lane in load i, and the tile column of its chunk
+    static __device__ __forceinline__ int k_of(int wave, int lane, int i) { return (wave * LD + i) * KPL + lane / CH; }
+    static __device__ __forceinline__ int col_of(int wave, int lane, int i) {
+        return ((lane % CH) ^ kc_swz<R>(k_of(wave, lane, i))) * 8;
+    }
+};
+
+// One MFMA operand (8 consecutive k of one column) from a KCols tile: two transposing
+// reads, k rows 4 apart.  `at`: the lane's element offset for column block j.
+template <int R>
+__device__ __forceinline__ int kc_at(int lane, int col0, int j) {
+    const int g = lane >> 4, sl = lane & 15;
+    const int kl = 8 * (g >> 1) + (sl >> 2), c = col0 + 32 * j + 16 * (g & 1) + 4 * (sl & 3);
+    return kl * R + (((c >> 3) ^ kc_swz<R>(kl)) << 3) + (c & 7);
+}
+template <int R>
+__device__ __forceinline__ u32x4 read_kcols(const u16* p0) {
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p0));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p0 + 4 * R));
+    const u32x2 l2 = __builtin_bit_cast(u32x2, lo);
+    const u32x2 h2 = __builtin_bit_cast(u32x2, hi);
+    return u32x4{l2[0], l2[1], h2[0], h2[1]};
+}
+
+// ------------------------------------------------------------------------------------
+// The tiled kernel over rows of groups: A rows [M,K] (through the row index, if any), B
+// [N,K] or [K,N].  WM x WN waves of (BM/WM) x (BN/WN), MFMA 32x32x16, ST stages.
+//   Step t waits until its tile has landed (the loads of up to ST-2 later tiles stay in
+//   flight) and meets the other waves, which have then also read all of tile t-1; sends
+//   the loads of tile t+ST-1 into the stage that tile left; and computes tile t.
+//   Loads past the last tile read nothing (zeros), so that every step has the same number
+//   of loads in flight.
+//   Epilogue: a wave stages 32 rows of its block at a time in LDS as fp32 and takes them
+//   back as runs of eight columns, so that bias, residual, stored z and C move in 16-byte
+//   pieces of whole row segments.
+// ------------------------------------------------------------------------------------
+template <int DT, int LAYOUT, int BM, int BN, int WM, int WN, int ST, int OCC>
+__global__ void __attribute__((amdgpu_flat_work_group_size(WM * WN * 64, WM * WN * 64),
+                               amdgpu_waves_per_eu(OCC, OCC)))
+fused_tiled(const FusedArgs p, int grid_n, int group_m) {
+    constexpr int NW = WM * WN, WTM = BM / WM, WTN = BN / WN, TM = WTM / 32, TN = WTN / 32;
+    constexpr int SLOT_A = BM * kTileK, STAGE = (BM + BN) * kTileK;   // elements
+    constexpr int SRF = WTN + 4;                                      // staged row in floats
+    static_assert(WTN % 64 == 0, "gate and up blocks of a pair in one wave");
+    static_assert(NW * 32 * SRF * 4 <= ST * STAGE * 2, "C staging fits the ring");
+    __shared__ __attribute__((aligned(1024))) u16 lds[ST * STAGE];
+    int g, row0, row_end, tn;
+    if (!find_tile<BM>(p, (int)blockIdx.x, grid_n, group_m, g, row0, row_end, tn))
+        return;
+    g = __builtin_amdgcn_readfirstlane(g);
+    row0 = __builtin_amdgcn_readfirstlane(row0);
+    row_end = __builtin_amdgcn_readfirstlane(row_end);
+    const int tid = (int)threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WN, wn = wave % WN, half = lane >> 5, lr = lane & 31;
+    const int K = p.K, nk = (K + kTileK - 1) / kTileK;
+
+    // A: rows of the tile from its first row on, or the whole of A through the row index
+    KRows<BM, NW> la;
+    const u16* a0 = p.row_index ? p.A : p.A + (int64_t)row0 * p.lda;
+    const int a_rows = p.row_index ? p.a_rows : (row_end - row0 < BM ? row_end - row0 : BM);
+    const rsrc4_t ra = make_rsrc4(a0, span_bytes(a_rows, K, p.lda));
+    la.init(wave, lane, [&](int r) -> uint32_t {
+        if (row0 + r >= row_end)
+            return kOutOfRange;
+        const int s = p.row_index ? a_row_of(p, row0 + r) : r;
+        return s < 0 ? kOutOfRange : (uint32_t)s * (uint32_t)p.lda * 2u;
+    });
+    const u16* b0 = p.B + (int64_t)g * p.stride_b;
+    const rsrc4_t rb = LAYOUT == LAYOUT_NK ? make_rsrc4(b0, span_bytes(p.N, K, p.ldb))
+                                           : make_rsrc4(b0, span_bytes(K, p.N, p.ldb));
+    using BC = KCols<BN, NW>;
+    KRows<BN, NW> lb;
+    uint32_t bo[BC::LD];
+    if constexpr (LAYOUT == LAYOUT_NK) {
+        lb.init(wave, lane, [&](int r) -> uint32_t {
+            const int n = b_row_of<BN>(p, tn, r);
+            return n < 0 ? kOutOfRange : (uint32_t)n * (uint32_t)p.ldb * 2u;
+        });
+    } else {
+#pragma unroll
+        for (int i = 0; i < BC::LD; ++i) {
+            const int n = b_row_of<BN>(p, tn, BC::col_of(wave, lane, i));
+            bo[i] = n < 0 ? kOutOfRange
+                          : ((uint32_t)BC::k_of(wave, lane, i) * (uint32_t)p.ldb + (uint32_t)n) * 2u;
+        }
+    }
+    const uint32_t lds0 = lds_addr(lds);
+    auto load = [&](int t, int slot) {
+        const int k0 = t * kTileK;
+        const uint32_t at = lds0 + (uint32_t)(slot * STAGE * 2);
+        la.load(ra, at, wave, k0, K);
+        if constexpr (LAYOUT == LAYOUT_NK) {
+            lb.load(rb, at + SLOT_A * 2, wave, k0, K);
+        } else {
+#pragma unroll
+            for (int i = 0; i < BC::LD; ++i)
+                dma16_at(rb, at + SLOT_A * 2 + (uint32_t)((wave * BC::LD + i) * 1024),
+                         k0 + BC::k_of(wave, lane, i) < K ? bo[i] : kOutOfRange,
+                         (uint32_t)(k0 < K ? k0 : 0) * (uint32_t)p.ldb * 2u);
+        }
+    };
+    constexpr int LOADS = KRows<BM, NW>::LD + BN / 8 / NW;
+
+    f32x16 acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            acc[i][j] = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+    const int xr = swz<8>(lr);
+    int kb[TN];
+    if constexpr (LAYOUT == LAYOUT_KN) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            kb[j] = kc_at<BN>(lane, wn * WTN, j);
+    }
+#pragma unroll
+    for (int t = 0; t < ST - 1; ++t)
+        load(t, t);
+    int slot = 0;
+    for (int t = 0; t < nk; ++t) {
+        wait_vm_then_sync<(ST - 2) * LOADS>();
+        load(t + ST - 1, slot == 0 ? ST - 1 : slot - 1);
+        const u16* as = lds + slot * STAGE + (wm * WTM + lr) * kTileK;
+        const u16* bs = lds + slot * STAGE + SLOT_A;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const int ko = (((2 * s) | half) ^ xr) * 8;
+            u32x4 fa[TM], fb[TN];
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                if constexpr (LAYOUT == LAYOUT_NK)
+                    fb[j] = *reinterpret_cast<const u32x4*>(bs + (wn * WTN + 32 * j + lr) * kTileK + ko);
+                else
+                    fb[j] = read_kcols<BN>(bs + kb[j] + 16 * s * BN);
+            }
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+                fa[i] = *reinterpret_cast<const u32x4*>(as + 32 * i * kTileK + ko);
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    acc[i][j] = mfma_32x32x16<DT>(fb[j], fa[i], acc[i][j]);
+        }
+        slot = slot + 1 == ST ? 0 : slot + 1;
+    }
+    wait_vm_then_sync<0>();            // no load writes LDS any more, no wave reads it
+
+    float* stage = reinterpret_cast<float*>(lds) + wave * 32 * SRF;
+    const int width = p.gated ? p.N >> 1 : p.N;
+    auto emit = [&](auto gatedc) {
+        constexpr bool GATED = decltype(gatedc)::value;
+        constexpr int RUNS = WTN / (GATED ? 16 : 8), RPI = 64 / RUNS, Q = 32 / RPI;
+        const int c = (lane % RUNS) * 8;
+        const int n = tn * (GATED ? BN / 2 : BN) + wn * (GATED ? WTN / 2 : WTN) + c;
+        const int zc = GATED ? (c >> 5) * 64 + (c & 31) : c;
+        float bz[8], bu[8];
+        load_bias<DT>(p, g, n, width, bz, bu);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            const int m0 = row0 + wm * WTM + i * 32 + lane / RUNS;
+            float r[Q][8] = {};
+            if (p.residual) {
+#pragma unroll
+                for (int q = 0; q < Q; ++q)
+                    if (m0 + q * RPI < row_end && n < width)
+                        load_residual<DT>(p, m0 + q * RPI, n, width, r[q]);
+            }
+            wave_lds_order();
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    *reinterpret_cast<f32x4*>(stage + lr * SRF + 32 * j + 8 * v + 4 * half) =
+                        f32x4{acc[i][j][4 * v], acc[i][j][4 * v + 1], acc[i][j][4 * v + 2], acc[i][j][4 * v + 3]};
+            wave_lds_order();
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                const float* src = stage + (q * RPI + lane / RUNS) * SRF + zc;
+                float z[8], u[8] = {};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    z[e] = src[e];
+                    if constexpr (GATED)
+                        u[e] = src[32 + e];
+                }
+                if (m0 + q * RPI < row_end && n < width)
+                    finish8<DT>(p, m0 + q * RPI, n, width, z, u, bz, bu, r[q]);
+            }
+        }
+    };
+    if (p.gated)
+        emit(std::true_type{});
+    else
+        emit(std::false_type{});
+}
+
+// ------------------------------------------------------------------------------------
+// The tiled kernel of the sums over a group's rows (sum_generic's products): both operands
+// have the summed row as their row index, so both are KCols tiles, read by transposing
+// reads.  An operand that goes through the row index has each tile's 64 indices fetched by
+// a direct-to-LDS load of its own, one tile ahead of the tile that needs them.
+// ------------------------------------------------------------------------------------
+__device__ __forceinline__ void dma4_at(rsrc4_t r, uint32_t lds_byte, uint32_t voff) {
+    const uint32_t m0v = __builtin_amdgcn_readfirstlane(lds_byte);
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
+                 ::"v"(voff), "s"(r), "s"(m0v)
+                 : "memory", "m0");
+}
+
+template <int DT, int BI, int BJ, int WI, int WJ, int ST, int OCC>
+__global__ void __attribute__((amdgpu_flat_work_group_size(WI * WJ * 64, WI * WJ * 64),
+                               amdgpu_waves_per_eu(OCC, OCC)))
+sum_tiled(const SumArgs p, int grid_i, int grid_j) {
+    constexpr int NW = WI * WJ, WTI = BI / WI, WTJ = BJ / WJ, TI = WTI / 32, TJ = WTJ / 32;
+    constexpr int SLOT_L = BI * kTileK, STAGE = (BI + BJ) * kTileK;
+    constexpr int SRS = WTJ + 8;                        // staged row in elements
+    static_assert(NW * 32 * SRS <= ST * STAGE, "D staging fits the ring");
+    __shared__ __attribute__((aligned(1024))) u16 lds[ST * STAGE];
+    __shared__ __attribute__((aligned(256))) int32_t idx[NW][2][64];
+    const int per = grid_i * grid_j, g = (int)blockIdx.x / per;
+    int ti, tj, lo, hi;
+    tile_of((int)blockIdx.x % per, grid_i, grid_j, 4, ti, tj);
+    group_rows(p, g, lo, hi);
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    hi = __builtin_amdgcn_readfirstlane(hi);
+    const int tid = (int)threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wi = wave / WJ, wj = wave % WJ, half = lane >> 5, lr = lane & 31;
+    const int K = hi - lo, nk = (K + kTileK - 1) / kTileK;
+    using LC = KCols<BI, NW>;
+    using RC = KCols<BJ, NW>;
+    const bool indexed = p.row_index != nullptr;
+    constexpr int LOADS = LC::LD + RC::LD;
+
+    const uint32_t lds0 = lds_addr(lds), idx0 = lds_addr(&idx[wave][0][0]);
+    const rsrc4_t rx = make_rsrc4(p.row_index + (indexed ? lo : 0), indexed ? (uint32_t)K * 4u : 0u);
+    auto load_idx = [&](int t) {
+        if (indexed)
+            dma4_at(rx, idx0 + (uint32_t)((t & 1) * 256), (uint32_t)(t * kTileK + lane) * 4u);
+    };
+    auto load = [&](int t, int slot) {
+        const int k0 = t * kTileK;
+        const uint32_t at = lds0 + (uint32_t)(slot * STAGE * 2);
+        auto operand = [&](auto cols, const u16* base, int ld, int limit, int col0, bool via, uint32_t lds_at) {
+            using C = decltype(cols);
+            // plain rows: a buffer over the tile's own rows, so the tail reads as zeros
+            const int rows = K - k0 < kTileK ? (K - k0 > 0 ? K - k0 : 0) : kTileK;
+            const rsrc4_t r = via ? make_rsrc4(base, span_bytes(p.a_rows, limit, ld))
+                                  : make_rsrc4(base + (int64_t)(lo + (rows > 0 ? k0 : 0)) * ld,
+                                               span_bytes(rows, limit, ld));
+#pragma unroll
+            for (int i = 0; i < C::LD; ++i) {
+                const int kk = C::k_of(wave, lane, i), n = col0 + C::col_of(wave, lane, i);
+                int row = kk;
+                bool ok = n < limit && kk < rows;
+                if (via) {
+                    const int v = idx[wave][t & 1][kk];
+                    row = p.row_div == 1 ? v : v / p.row_div;
+                    ok = ok && v >= 0 && row < p.a_rows;
+                }
+                dma16_at(r, lds_at + (uint32_t)((wave * C::LD + i) * 1024),
+                         ok ? ((uint32_t)row * (uint32_t)ld + (uint32_t)n) * 2u : kOutOfRange, 0u);
+            }
+        };
+        operand(LC{}, p.left, p.ldl, p.I, ti * BI, p.index_left, at);
+        operand(RC{}, p.right, p.ldr, p.J, tj * BJ, p.index_right, at + SLOT_L * 2);
+    };
+
+    f32x16 acc[TI][TJ];
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int j = 0; j < TJ; ++j)
+            acc[i][j] = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+    int la[TI], ra[TJ];
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+        la[i] = kc_at<BI>(lane, wi * WTI, i);
+#pragma unroll
+    for (int j = 0; j < TJ; ++j)
+        ra[j] = kc_at<BJ>(lane, wj * WTJ, j);
+    // a wave reads the indices that it loaded itself: its own wait is enough
+    load_idx(0);
+    load_idx(1);
+    wait_vm<0>();
+    if (nk > 0) {
+#pragma unroll
+        for (int t = 0; t < ST - 1; ++t) {
+            load(t, t);
+            wave_lds_order();          // the indices of tile t are read
+            load_idx(t + 2);
+            if (indexed)
+                wait_vm<0>();
+        }
+    }
+    int slot = 0;
+    for (int t = 0; t < nk; ++t) {
+        // in flight past this point: the tiles t+1 .. t+ST-2 and, indexed, the indices that
+        // were sent after tile t+ST-2 (so that waiting for tile t+ST-2's would be needed
+        // only if they were older: loads complete in order)
+        if constexpr (ST == 2) {
+            wait_vm_then_sync<0>();
+        } else {
+            if (indexed)
+                wait_vm_then_sync<0>();
+            else
+                wait_vm_then_sync<(ST - 2) * LOADS>();
+        }
+        load(t + ST - 1, slot == 0 ? ST - 1 : slot - 1);
+        if (indexed) {
+            wave_lds_order();
+            load_idx(t + ST + 1);
+        }
+        const u16* ls = lds + slot * STAGE;
+        const u16* rs = ls + SLOT_L;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            u32x4 fl[TI], fr[TJ];
+#pragma unroll
+            for (int j = 0; j < TJ; ++j)
+                fr[j] = read_kcols<BJ>(rs + ra[j] + 16 * s * BJ);
+#pragma unroll
+            for (int i = 0; i < TI; ++i)
+                fl[i] = read_kcols<BI>(ls + la[i] + 16 * s * BI);
+#pragma unroll
+            for (int i = 0; i < TI; ++i)
+#pragma unroll
+                for (int j = 0; j < TJ; ++j)
+                    acc[i][j] = mfma_32x32x16<DT>(fr[j], fl[i], acc[i][j]);
+        }
+        slot = slot + 1 == ST ? 0 : slot + 1;
+    }
+    wait_vm_then_sync<0>();
+    // D: 32 rows at a time through LDS, 16 bytes per lane of whole row segments
+    u16* stage = lds + wave * 32 * SRS;
+    constexpr int RUNS = WTJ / 8, RPI = 64 / RUNS;
+    const int j0 = tj * BJ + wj * WTJ + (lane % RUNS) * 8;
+    u16* D = p.D + (int64_t)g * p.stride_d;
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+        wave_lds_order();
+#pragma unroll
+        for (int j = 0; j < TJ; ++j)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                *reinterpret_cast<u32x2*>(stage + lr * SRS + 32 * j + 8 * v + 4 * half) =
+                    u32x2{pack2<DT>(acc[i][j][4 * v], acc[i][j][4 * v + 1]),
+                          pack2<DT>(acc[i][j][4 * v + 2], acc[i][j][4 * v + 3])};
+        wave_lds_order();
+#pragma unroll
+        for (int q = 0; q < 32 / RPI; ++q) {
+            const int r = q * RPI + lane / RUNS, row = ti * BI + wi * WTI + 32 * i + r;
+            const u32x4 v = *reinterpret_cast<const u32x4*>(stage + r * SRS + (lane % RUNS) * 8);
+            if (row < p.I && j0 < p.J) {
+                u16* q0 = D + (int64_t)row * p.ldd + j0;
+                if (p.vec && j0 + 8 <= p.J) {
+                    *reinterpret_cast<u32x4*>(q0) = v;
+                } else {
+                    const u16x8 h = __builtin_bit_cast(u16x8, v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (j0 + e < p.J)
+                            q0[e] = h[e];
+                }
+            }
+        }
+    }
+}
+
+}  // namespace tgemm
