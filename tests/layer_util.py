@@ -104,8 +104,12 @@ def check_layer(got, z, kind, gated, residual, what):
     roundings (product with the gate, residual) and the rounding of C."""
     y = layer(z, kind, gated)
     want = y if residual is None else y + residual
+    # gelu below -6: the kernel's Phi(-a) follows its own fall-off there, and a Phi(-a) times
+    # its relative error (3.4e-5 at 6.5, 3.9e-4 at 7, 1.9e-3 at 7.5, 4e-2 at 9, 1 past 13) is
+    # below 1e-14 everywhere
+    far = 1e-14 * (z[:, z.shape[1] // 2:].abs() if gated else 1.0) if kind == ACT_GELU else 0.0
     # |z| below 2^-20 cannot occur (multiples of 1/128), so the activation's relative bound
     # holds; where it has decayed below 1e-30 the fp32 form may flush
     inner = (0 if kind in (ACT_NONE, ACT_RELU) else ACT_ERROR) * y.abs() + 1e-30
-    inner = inner + 2.0 ** -23 * (y.abs() + want.abs())
+    inner = inner + far + 2.0 ** -23 * (y.abs() + want.abs())
     assert_within(got, want, half_step(got.dtype, want) + 1.01 * inner, what)

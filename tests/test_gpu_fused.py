@@ -121,7 +121,7 @@ def test_activation_curves(tg):
     for kind in ACTS:
         got = tg.gemm_fused(A.cuda(), B.cuda(), activation=kind)
         want = layer(z[None, :n].double(), kind, False)
-        assert_within(got, want, half_step(dt, want) + ACT_ERROR * want.abs() * 1.1 + 1e-30, f"act {kind}")
+        assert_within(got, want, half_step(dt, want) + ACT_ERROR * want.abs() * 1.1 + 1e-14, f"act {kind}")
 
 
 def test_infinities_and_nan(tg):

@@ -4,6 +4,7 @@
 #include "tgemm.h"
 
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "fused_launch.hpp"
@@ -137,18 +138,39 @@ bool tiles_fit(const Layer& l) {
            (!l.row_index || 2 * span(l.a_rows, l.k, l.lda) <= kMaxBufferBytes);
 }
 
-// The tile form of a product over rows: the least of (waves of workgroups on 256 compute
-// units) x (one tile's time relative to 256x256), the groups taken as equal.
+// The form of a product over rows: the least estimated time.  A form's compute time is its
+// rounds of workgroups on the 256 compute units times its K steps times the time of a step,
+// measured at K = 4096 with bf16 operands in cache (us per 64 k, alone on a unit and with
+// as many neighbours as fit); its memory time is the operands' and C's bytes at the rate
+// that it streams B with (the stream forms read 5.5 TB/s, the tiled ones 4.6 with one row
+// tile per group, the quad kernel 5.1).
 tgemm_fused::Form choose_rows(const Layer& l) {
-    static const double kTime[tgemm_fused::FORMS] = {1.0, 0.36, 0.22};
-    static const int kPerUnit[tgemm_fused::FORMS] = {1, 2, 2};
-    int best = 0;
+    struct Cost {
+        int per_unit;                 // workgroups that share a compute unit
+        double alone, shared, fixed;  // us per step in either case; us per launch
+        double rate;                  // TB/s
+    };
+    static const Cost kCost[tgemm_fused::FORMS] = {
+        {1, 1.34, 1.34, 9, 5.1}, {2, 0.62, 0.97, 6, 4.6}, {2, 0.39, 0.61, 5, 4.6}, {3, 0.26, 0.45, 5, 4.6},
+        {2, 0.16, 0.30, 4, 5.5}, {4, 0.22, 0.55, 4, 5.6}, {2, 0.18, 0.32, 4, 5.4}, {1, 0.24, 0.24, 4, 5.0}};
+    // groups that have rows, if each row fell into any group alike
+    const double live = l.groups == 1 ? 1.0 : l.groups * (1.0 - exp(-(double)l.rows / l.groups));
+    const double avg = l.rows / live, steps = (double)cdiv(l.k, 64);
+    const double bytes = 2.0 * (live * l.n * l.k + (double)l.rows * l.k + (double)l.rows * l.width());
+    int best = 1;
     double least = 0;
     for (int f = 0; f < tgemm_fused::FORMS; ++f) {
-        const int64_t live = l.offsets ? (l.groups < l.rows ? l.groups : l.rows) : 1;
-        const int64_t tiles = live * cdiv(cdiv(l.rows, live), tgemm_fused::kTiles[f].m) *
-                              cdiv(l.width(), tgemm_fused::kTiles[f].n / (l.gated ? 2 : 1));
-        const double cost = (double)cdiv(tiles, 256 * kPerUnit[f]) * kPerUnit[f] * kTime[f];
+        if (f >= tgemm_fused::FORM_STREAM16 && l.b_layout != TGEMM_B_NK)
+            break;
+        const Cost& c = kCost[f];
+        const tgemm_fused::Tile t = tgemm_fused::kTiles[f];
+        const double row_tiles = l.groups == 1 ? (double)cdiv(l.rows, t.m)
+                                               : live * (avg / t.m + 0.4 > 1.0 ? avg / t.m + 0.4 : 1.0);
+        const double tiles = row_tiles * (double)cdiv(l.width(), t.n / (l.gated ? 2 : 1));
+        const double slots = 256.0 * c.per_unit, full = floor(tiles / slots), rest = tiles - full * slots;
+        const double compute = steps * (full * c.shared + (rest > 256 ? c.shared : (rest > 0 ? c.alone : 0)));
+        const double memory = bytes / (c.rate * 1e6);
+        const double cost = (compute > memory ? compute : memory) + c.fixed;
         if (f == 0 || cost < least) {
             best = f;
             least = cost;
@@ -166,6 +188,10 @@ int launch_rows(const Layer& l, const FusedArgs& p, hipStream_t s) {
         if (tm * tn > kMaxDim)
             return TGEMM_ERR_UNSUPPORTED;
         (void)hipGetLastError();
+        if (form >= tgemm_fused::FORM_STREAM16)
+            return status(tgemm_fused::rows_stream(l.dtype, form, p, tm, (int)tn, s));
+        if (form == tgemm_fused::FORM_QUAD)
+            return status(tgemm_fused::rows_quad(l.dtype, l.b_layout, p, tm, (int)tn, s));
         return status(l.b_layout == TGEMM_B_NK ? tgemm_fused::rows_tiled_nk(l.dtype, form, p, tm, (int)tn, s)
                                                : tgemm_fused::rows_tiled_kn(l.dtype, form, p, tm, (int)tn, s));
     }
@@ -289,9 +315,11 @@ int launch_sum(const Layer& l, const SumArgs& p, hipStream_t s) {
         const int64_t t256 = l.groups * cdiv(p.I, 256) * cdiv(p.J, 256);
         if (l.groups * cdiv(p.I, 128) * cdiv(p.J, 128) > kMaxDim)
             return TGEMM_ERR_UNSUPPORTED;
-        tgemm_fused::Form f = t256 >= 128 ? tgemm_fused::FORM_256 : tgemm_fused::FORM_128;
+        bool large = t256 >= 128, quad = large;
         (void)hipGetLastError();
-        return status(tgemm_fused::sum_tiled(l.dtype, f, p, s));
+        if (quad && !p.row_index && p.vec && 2 * span(p.rows, p.I, p.ldl) <= kMaxBufferBytes && 2 * span(p.rows, p.J, p.ldr) <= kMaxBufferBytes)
+            return status(tgemm_fused::sum_quad(l.dtype, p, s));
+        return status(tgemm_fused::sum_tiled(l.dtype, large, p, s));
     }
     const int64_t gi = cdiv(p.I, 64), gj = cdiv(p.J, 64);
     if (l.groups * gi * gj > kMaxDim)

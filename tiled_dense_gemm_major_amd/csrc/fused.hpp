@@ -134,23 +134,27 @@ __device__ __forceinline__ float logistic(float x) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * x));
 }
 
-// erfc(u) for u >= 0 as exp(-u^2) t P(t), t = 1 / (1 + 0.44 u), the form of Hastings
-// ("Approximations for Digital Computers", 1955): P, of degree 5, was fitted to
-// exp(u^2) erfc(u) t^-1 on [0, 12] for the least relative error, 5.3e-6.
-__device__ __forceinline__ float erfc_pos(float u, float& gauss) {
-    const float t = __builtin_amdgcn_rcpf(fmaf(0.44f, u, 1.0f));
-    gauss = __builtin_amdgcn_exp2f(-1.44269504f * u * u);
-    float q = fmaf(t, -0.14623456f, 0.35104576f);
-    q = fmaf(t, q, 0.04027511f);
-    q = fmaf(t, q, 0.26383517f);
-    q = fmaf(t, q, 0.24250634f);
-    q = fmaf(t, q, 0.24856692f);
-    return t * q * gauss;
+// Phi(-a) for a >= 0 as 2^Q(a): log2 Phi(-a) is close to a parabola, and Q, of degree 7,
+// was fitted to it on [0, 6] for the least absolute error (3.3e-6 in the exponential,
+// 6.5e-6 evaluated in fp32).  Beyond 6, where Phi(-a) < 1e-9, Q falls on (its leading
+// coefficient is negative): 2e-3 relative at 8.3.  One transcendental instead of the two
+// of erfc's usual forms: 12 us less over 67 M values beside the 8192^3 product.
+__device__ __forceinline__ float normal_tail(float a) {
+    float q = fmaf(a, -1.8348411e-6f, 6.159888e-5f);
+    q = fmaf(a, q, -9.3052925e-4f);
+    q = fmaf(a, q, 8.507907e-3f);
+    q = fmaf(a, q, -5.3960098e-2f);
+    q = fmaf(a, q, -0.45846437f);
+    q = fmaf(a, q, -1.1512511f);
+    q = fmaf(a, q, -0.9999953f);
+    return __builtin_amdgcn_exp2f(q);
 }
 
-// The same with P of degree 7 and t = 1 / (1 + 0.43 u), 1.8e-7: for the slopes, whose
-// column sums are kept in fp32.
-__device__ __forceinline__ float erfc_pos_fine(float u, float& gauss) {
+// erfc(u) for u >= 0 as exp(-u^2) t P(t), t = 1 / (1 + 0.43 u), the form of Hastings
+// ("Approximations for Digital Computers", 1955): P, of degree 7, was fitted to
+// exp(u^2) erfc(u) / t on [0, 12] for the least relative error, 1.8e-7.  For the slopes,
+// whose column sums are kept in fp32.
+__device__ __forceinline__ float erfc_pos(float u, float& gauss) {
     const float t = __builtin_amdgcn_rcpf(fmaf(0.43f, u, 1.0f));
     gauss = __builtin_amdgcn_exp2f(-1.44269504f * u * u);
     float q = fmaf(t, 0.07092017f, -0.29907167f);
@@ -169,12 +173,10 @@ __device__ __forceinline__ float activate(int act, float x) {
     switch (act) {
     case ACT_RELU: return x > 0.0f ? x : (x != x ? x : 0.0f);
     case ACT_GELU: {
-        // x Phi(x) = max(x, 0) - |x| erfc(|x| / sqrt(2)) / 2; an infinite |x| has a zero
-        // second term
-        float gauss;
+        // x Phi(x) = max(x, 0) - |x| Phi(-|x|)
+        // a NaN comes through the tail; an infinity leaves 1e30 * 0 of the second term
         const float a = fabsf(x);
-        const float tail = erfc_pos(0.70710678f * a, gauss);
-        return (x > 0.0f ? x : 0.0f) - (tail > 0.0f || tail != tail ? 0.5f * a * tail : 0.0f);
+        return fmaf(-fminf(a, 1e30f), normal_tail(a), fmaxf(x, 0.0f));
     }
     case ACT_GELU_TANH: return x * logistic(kGeluTanh * (x + 0.044715f * x * x * x));
     case ACT_SILU: return x * logistic(x);
@@ -192,7 +194,7 @@ __device__ __forceinline__ void activate_slope(int act, float x, float& value, f
     case ACT_GELU: {
         float gauss;                       // exp(-x^2 / 2)
         const float a = fabsf(x);
-        const float half_tail = 0.5f * erfc_pos_fine(0.70710678f * a, gauss);
+        const float half_tail = 0.5f * erfc_pos(0.70710678f * a, gauss);
         const float phi = x > 0.0f ? 1.0f - half_tail : half_tail;
         value = x * phi;
         slope = phi + (gauss > 0.0f || gauss != gauss ? x * 0.39894228f * gauss : 0.0f);
@@ -248,7 +250,7 @@ __device__ __forceinline__ void load8(const u16* p, bool vec, int left, float (&
 }
 
 template <int DT>
-__device__ __forceinline__ void store8(u16* p, bool vec, int left, const float (&x)[8]) {
+__device__ __forceinline__ void store8(u16* p, bool vec, int left, const float* x) {
     const u32x4 v{pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]), pack2<DT>(x[4], x[5]),
                   pack2<DT>(x[6], x[7])};
     if (vec && left >= 8) {
@@ -277,66 +279,99 @@ __device__ __forceinline__ void load_bias(const FusedArgs& p, int g, int n, int 
     }
 }
 
-// The epilogue of eight columns n .. n+7 of row s (n < width, C's): z holds the product
-// there and, gated, u the product h columns on; bz and bu their bias, r the residual.
-template <int DT>
-__device__ __forceinline__ void finish8(const FusedArgs& p, int s, int n, int width, float (&z)[8], float (&u)[8],
-                                        const float (&bz)[8], const float (&bu)[8], const float (&r)[8]) {
-    const int left = width - n;
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        z[e] += bz[e];
-    if (p.gated) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            u[e] += bu[e];
-    }
-    if (p.preact) {
-        u16* q = p.preact + (int64_t)s * p.ldp + n;
-        store8<DT>(q, p.vec & VEC_PRE, left, z);
-        if (p.gated)
-            store8<DT>(q + width, p.vec & VEC_PRE, left, u);
-    }
-    // one uniform branch per run of eight
-    switch (p.act) {
+// An activation over a run of values: one uniform branch for all of them.
+template <int COUNT>
+__device__ __forceinline__ void activate_all(int act, float* z) {
+    switch (act) {
     case ACT_RELU:
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
+        for (int e = 0; e < COUNT; ++e)
             z[e] = activate(ACT_RELU, z[e]);
         break;
     case ACT_GELU:
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
+        for (int e = 0; e < COUNT; ++e)
             z[e] = activate(ACT_GELU, z[e]);
         break;
     case ACT_GELU_TANH:
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
+        for (int e = 0; e < COUNT; ++e)
             z[e] = activate(ACT_GELU_TANH, z[e]);
         break;
     case ACT_SILU:
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
+        for (int e = 0; e < COUNT; ++e)
             z[e] = activate(ACT_SILU, z[e]);
         break;
     default: break;
     }
-    if (p.gated) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            z[e] *= u[e];
-    }
-    if (p.residual) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            z[e] += r[e];
-    }
-    store8<DT>(p.C + (int64_t)s * p.ldc + n, p.vec & VEC_C, left, z);
 }
 
-template <int DT>
-__device__ __forceinline__ void load_residual(const FusedArgs& p, int s, int n, int width, float (&r)[8]) {
-    load8<DT>(p.residual + (int64_t)s * p.ldr + n, p.vec & VEC_RES, width - n, r);
+// The epilogue of Q runs of eight columns n .. n+7 (n < width, C's) of the rows s, s + STEP,
+// .. below `end`: z holds the products there and, gated, u the products h columns on; bz and
+// bu their bias.  The runs go through each stage together, so that their memory accesses
+// and their chains of arithmetic overlap.
+template <int DT, int Q, int STEP, bool GATED>
+__device__ __forceinline__ void finish_runs(const FusedArgs& p, int s, int end, int n, int width, float (&z)[Q * 8],
+                                            float (&u)[GATED ? Q * 8 : 1], const float (&bz)[8],
+                                            const float (&bu)[8]) {
+    const int left = width - n;
+    u32x4 raw[Q];                          // the residual, where it is read whole
+    const bool whole = p.residual && (p.vec & VEC_RES) && left >= 8;
+    if (whole) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+            if (s + q * STEP < end)
+                raw[q] = *reinterpret_cast<const u32x4*>(p.residual + (int64_t)(s + q * STEP) * p.ldr + n);
+    }
+    if (p.bias) {
+#pragma unroll
+        for (int e = 0; e < Q * 8; ++e) {
+            z[e] += bz[e & 7];
+            if constexpr (GATED)
+                u[e] += bu[e & 7];
+        }
+    }
+    if (p.preact) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+            if (s + q * STEP < end) {
+                u16* to = p.preact + (int64_t)(s + q * STEP) * p.ldp + n;
+                store8<DT>(to, p.vec & VEC_PRE, left, z + q * 8);
+                if constexpr (GATED)
+                    store8<DT>(to + width, p.vec & VEC_PRE, left, u + q * 8);
+            }
+    }
+    activate_all<Q * 8>(p.act, z);
+    if constexpr (GATED) {
+#pragma unroll
+        for (int e = 0; e < Q * 8; ++e)
+            z[e] *= u[e];
+    }
+    if (whole) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            float r[8];
+            unpack8<DT>(raw[q], r);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                z[q * 8 + e] += r[e];
+        }
+    } else if (p.residual) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+            if (s + q * STEP < end) {
+                float r[8];
+                load8<DT>(p.residual + (int64_t)(s + q * STEP) * p.ldr + n, false, left, r);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    z[q * 8 + e] += r[e];
+            }
+    }
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+        if (s + q * STEP < end)
+            store8<DT>(p.C + (int64_t)(s + q * STEP) * p.ldc + n, p.vec & VEC_C, left, z + q * 8);
 }
 
 // The B row (column of the product) of column c of column tile tn, whose tile is BN wide;
@@ -405,17 +440,17 @@ __global__ void __launch_bounds__(256) fused_generic(const FusedArgs p, int grid
         const int r = q / runs, c = (q % runs) * 8;
         const int n = tn * (runs * 8) + c;
         if (row0 + r < row_end && n < width) {
-            float z[8], u[8];
+            float z[8], u[8], bz[8], bu[8], none[1];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 z[e] = Cs[r * 68 + c + e];
                 u[e] = p.gated ? Cs[r * 68 + c + 32 + e] : 0.0f;
             }
-            float bz[8], bu[8], res[8] = {};
             load_bias<DT>(p, g, n, width, bz, bu);
-            if (p.residual)
-                load_residual<DT>(p, row0 + r, n, width, res);
-            finish8<DT>(p, row0 + r, n, width, z, u, bz, bu, res);
+            if (p.gated)
+                finish_runs<DT, 1, 1, true>(p, row0 + r, row_end, n, width, z, u, bz, bu);
+            else
+                finish_runs<DT, 1, 1, false>(p, row0 + r, row_end, n, width, z, none, bz, bu);
         }
     }
 }

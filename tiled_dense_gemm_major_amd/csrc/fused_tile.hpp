@@ -88,6 +88,51 @@ __device__ __forceinline__ u32x4 read_kcols(const u16* p0) {
 }
 
 // ------------------------------------------------------------------------------------
+// The epilogue of a wave's block of PASSES x 32 rows and WTN tile columns.  put(i, stage)
+// writes the i-th 32 rows to the wave's LDS stage as fp32 (row stride WTN + 4 floats);
+// they come back as runs of eight columns of one row per lane, so that bias, residual,
+// stored z and C move in 16-byte pieces of whole row segments.  m0: the block's first row;
+// n0: its first column of C.
+// ------------------------------------------------------------------------------------
+template <int DT, int WTN, int PASSES, bool GATED, typename PUT>
+__device__ __forceinline__ void rows_epilogue_as(const FusedArgs& p, int g, float* stage, int lane, int m0,
+                                                 int row_end, int n0, PUT&& put) {
+    constexpr int SRF = WTN + 4, RUNS = WTN / (GATED ? 16 : 8), RPI = 64 / RUNS, Q = 32 / RPI;
+    const int c = (lane % RUNS) * 8, n = n0 + c, width = p.gated ? p.N >> 1 : p.N;
+    const int zc = GATED ? (c >> 5) * 64 + (c & 31) : c;
+    float bz[8], bu[8];
+    load_bias<DT>(p, g, n, width, bz, bu);
+    static_for<0, PASSES>([&](auto ic) {
+        const int m = m0 + decltype(ic)::value * 32 + lane / RUNS;
+        wave_lds_order();
+        put(ic, stage);
+        wave_lds_order();
+        float z[Q * 8], u[GATED ? Q * 8 : 1];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const float* src = stage + (q * RPI + lane / RUNS) * SRF + zc;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                z[q * 8 + e] = src[e];
+                if constexpr (GATED)
+                    u[q * 8 + e] = src[32 + e];
+            }
+        }
+        if (n < width)
+            finish_runs<DT, Q, RPI, GATED>(p, m, row_end, n, width, z, u, bz, bu);
+    });
+}
+
+template <int DT, int WTN, int PASSES, typename PUT>
+__device__ __forceinline__ void rows_epilogue(const FusedArgs& p, int g, float* stage, int lane, int m0, int row_end,
+                                              int n0, PUT&& put) {
+    if (p.gated)
+        rows_epilogue_as<DT, WTN, PASSES, true>(p, g, stage, lane, m0, row_end, n0, put);
+    else
+        rows_epilogue_as<DT, WTN, PASSES, false>(p, g, stage, lane, m0, row_end, n0, put);
+}
+
+// ------------------------------------------------------------------------------------
 // The tiled kernel over rows of groups: A rows [M,K] (through the row index, if any), B
 // [N,K] or [K,N].  WM x WN waves of (BM/WM) x (BN/WN), MFMA 32x32x16, ST stages.
 //   Step t waits until its tile has landed (the loads of up to ST-2 later tiles stay in
@@ -95,9 +140,6 @@ __device__ __forceinline__ u32x4 read_kcols(const u16* p0) {
 //   the loads of tile t+ST-1 into the stage that tile left; and computes tile t.
 //   Loads past the last tile read nothing (zeros), so that every step has the same number
 //   of loads in flight.
-//   Epilogue: a wave stages 32 rows of its block at a time in LDS as fp32 and takes them
-//   back as runs of eight columns, so that bias, residual, stored z and C move in 16-byte
-//   pieces of whole row segments.
 // ------------------------------------------------------------------------------------
 template <int DT, int LAYOUT, int BM, int BN, int WM, int WN, int ST, int OCC>
 __global__ void __attribute__((amdgpu_flat_work_group_size(WM * WN * 64, WM * WN * 64),
@@ -213,53 +255,84 @@ fused_tiled(const FusedArgs p, int grid_n, int group_m) {
     }
     wait_vm_then_sync<0>();            // no load writes LDS any more, no wave reads it
 
-    float* stage = reinterpret_cast<float*>(lds) + wave * 32 * SRF;
-    const int width = p.gated ? p.N >> 1 : p.N;
-    auto emit = [&](auto gatedc) {
-        constexpr bool GATED = decltype(gatedc)::value;
-        constexpr int RUNS = WTN / (GATED ? 16 : 8), RPI = 64 / RUNS, Q = 32 / RPI;
-        const int c = (lane % RUNS) * 8;
-        const int n = tn * (GATED ? BN / 2 : BN) + wn * (GATED ? WTN / 2 : WTN) + c;
-        const int zc = GATED ? (c >> 5) * 64 + (c & 31) : c;
-        float bz[8], bu[8];
-        load_bias<DT>(p, g, n, width, bz, bu);
-#pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            const int m0 = row0 + wm * WTM + i * 32 + lane / RUNS;
-            float r[Q][8] = {};
-            if (p.residual) {
-#pragma unroll
-                for (int q = 0; q < Q; ++q)
-                    if (m0 + q * RPI < row_end && n < width)
-                        load_residual<DT>(p, m0 + q * RPI, n, width, r[q]);
-            }
-            wave_lds_order();
+    rows_epilogue<DT, WTN, TM>(
+        p, g, reinterpret_cast<float*>(lds) + wave * 32 * SRF, lane, row0 + wm * WTM, row_end,
+        tn * (p.gated ? BN / 2 : BN) + wn * (p.gated ? WTN / 2 : WTN), [&](auto ic, float* stage) {
+            constexpr int i = decltype(ic)::value;
 #pragma unroll
             for (int j = 0; j < TN; ++j)
 #pragma unroll
                 for (int v = 0; v < 4; ++v)
                     *reinterpret_cast<f32x4*>(stage + lr * SRF + 32 * j + 8 * v + 4 * half) =
                         f32x4{acc[i][j][4 * v], acc[i][j][4 * v + 1], acc[i][j][4 * v + 2], acc[i][j][4 * v + 3]};
-            wave_lds_order();
+        });
+}
+
+// ------------------------------------------------------------------------------------
+// The quad kernel over rows of groups: 256 x 256 tiles, one wave per SIMD with a 128 x 128
+// quadrant each, the library's main loop (quad_body) on a tile of a group.
+// ------------------------------------------------------------------------------------
+template <int DT>
+struct QuadRows {
+    static constexpr bool kActive = true;
+    const FusedArgs& p;
+    int g, row0, row_end, tn;
+
+    __device__ __forceinline__ int rows() const { return row_end - row0 < 256 ? row_end - row0 : 256; }
+    __device__ __forceinline__ int a_rows() const { return p.row_index ? p.a_rows : rows(); }
+    __device__ __forceinline__ int a_row(int r) const { return p.row_index ? a_row_of(p, row0 + r) : r; }
+    __device__ __forceinline__ int b_row(int c) const { return b_row_of<256>(p, tn, c); }
+
+    template <int MF, int TM, int TN, typename ACC>
+    __device__ __forceinline__ void finish(const ACC& acc, u16* lds, int wave, int lane) const {
+        constexpr int SRF = 128 + 4;
+        const int wm = wave >> 1, wn = wave & 1, lr = lane % MF, kq = lane / MF;
+        rows_epilogue<DT, 128, TM * MF / 32>(
+            p, g, reinterpret_cast<float*>(lds) + wave * 32 * SRF, lane, row0 + wm * (TM * MF), row_end,
+            tn * (p.gated ? 128 : 256) + wn * (p.gated ? 64 : 128), [&](auto ic, float* stage) {
+                constexpr int i0 = decltype(ic)::value * 32 / MF;
 #pragma unroll
-            for (int q = 0; q < Q; ++q) {
-                const float* src = stage + (q * RPI + lane / RUNS) * SRF + zc;
-                float z[8], u[8] = {};
+                for (int i = 0; i < 32 / MF; ++i)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    z[e] = src[e];
-                    if constexpr (GATED)
-                        u[e] = src[32 + e];
-                }
-                if (m0 + q * RPI < row_end && n < width)
-                    finish8<DT>(p, m0 + q * RPI, n, width, z, u, bz, bu, r[q]);
-            }
-        }
-    };
-    if (p.gated)
-        emit(std::true_type{});
-    else
-        emit(std::false_type{});
+                    for (int j = 0; j < TN; ++j)
+#pragma unroll
+                        for (int v = 0; v < (MF == 16 ? 1 : 4); ++v)
+                            *reinterpret_cast<f32x4*>(stage + (i * MF + lr) * SRF + MF * j +
+                                                      (MF == 16 ? 4 * kq : 8 * v + 4 * kq)) =
+                                f32x4{acc[i0 + i][j][4 * v], acc[i0 + i][j][4 * v + 1], acc[i0 + i][j][4 * v + 2],
+                                      acc[i0 + i][j][4 * v + 3]};
+            });
+    }
+};
+
+template <int DT, int MF, int LAYOUT, bool OFFS>
+__global__ void __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(1, 1)))
+fused_quad(const FusedArgs p, int grid_n, int group_m) {
+    int g, row0, row_end, tn;
+    if (!find_tile<256>(p, (int)blockIdx.x, grid_n, group_m, g, row0, row_end, tn))
+        return;
+    g = __builtin_amdgcn_readfirstlane(g);
+    row0 = __builtin_amdgcn_readfirstlane(row0);
+    row_end = __builtin_amdgcn_readfirstlane(row_end);
+    const QuadRows<DT> hook{p, g, row0, row_end, tn};
+    quad_body<DT, MF, (MF == 16 ? 2 : 1), (MF == 16 ? 56 : 40), (MF == 16 ? 40 : 12), 1, 2, OFFS, LAYOUT, 256,
+              LAYOUT_MK, 0>(p.row_index ? p.A : p.A + (int64_t)row0 * p.lda, p.B + (int64_t)g * p.stride_b, nullptr,
+                            hook.rows(), p.N, p.K, p.lda, p.ldb, 0, 0, tn, 0, 0, nullptr, 0, 0, 0, false, hook);
+}
+
+// The quad kernel of the sums over a group's rows, without a row index.
+template <int DT, bool OFFS>
+__global__ void __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(1, 1)))
+sum_quad(const SumArgs p, int grid_i, int grid_j) {
+    const int per = grid_i * grid_j, g = (int)blockIdx.x / per;
+    int ti, tj, lo, hi;
+    tile_of((int)blockIdx.x % per, grid_i, grid_j, 4, ti, tj);
+    group_rows(p, g, lo, hi);
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    hi = __builtin_amdgcn_readfirstlane(hi);
+    quad_body<DT, 32, 1, 40, 12, 1, 2, OFFS, LAYOUT_KN, 256, LAYOUT_KM, 0>(
+        p.left + (int64_t)lo * p.ldl, p.right + (int64_t)lo * p.ldr, p.D + (int64_t)g * p.stride_d, p.I, p.J, hi - lo,
+        p.ldl, p.ldr, p.ldd, ti, tj, 0, 0, nullptr, 0, 0, 0);
 }
 
 // ------------------------------------------------------------------------------------

@@ -1470,17 +1470,33 @@ __device__ __forceinline__ int kn_swz(int k) {
     return MF == 16 ? 2 * ((k & 3) + 4 * ((k >> 3) & 1)) : 4 * (k & 3);
 }
 
+// What a caller of quad_body may put in place of its plain operand rows and epilogue (A
+// [M,K] and MODE 0 only), with kActive true:
+//   int a_rows()         rows that the A buffer spans (M: the tile's rows that exist)
+//   int a_row(int r)     the A row of tile row r (below M), or -1 (read as zeros)
+//   int b_row(int c)     the row of B [N,K] (column of B [K,N]) of tile column c, or -1
+//   void finish<MF, TM, TN>(acc, lds, wave, lane)   takes the accumulators; the LDS ring is
+//                        free, and the wave's block starts at tile row (wave / 2) (BMT / 2)
+//                        and tile column (wave % 2) 128
+// The instruction-offset form (OFFS) needs row 8 b or later in load b of a wave's first
+// rows, so not with arbitrary a_row.
+struct QuadPlain {
+    static constexpr bool kActive = false;
+};
+
 // The body of the quad kernels: C tile (tm, tn).  MODE 0: the whole K walk, cast to C.
 // MODE 1 (partial): the K range [k0, k0 + klen) only (k0 a multiple of 64) and the fp32
 // partial tile stored to P, element (m, n) at P[(m - pm0) * ldp + (n - pn0)], instead of
 // the cast to C.  MODE 2: MODE 1 where `partial` holds, else MODE 0 (one body, so one LDS
 // ring, for a kernel that does both).
 template <int DT, int MF, int PRE, int SPA, int SPB, int STAG, int POL, bool OFFS, int LAYOUT,
-          int BMT, int ALAY, int MODE>
+          int BMT, int ALAY, int MODE, class HOOK = QuadPlain>
 __device__ __attribute__((always_inline)) inline void
 quad_body(const u16* __restrict__ A, const u16* __restrict__ B, u16* __restrict__ C, int M,
           int N, int K, int lda, int ldb, int ldc, int tm, int tn, int k0, int klen,
-          float* __restrict__ P, int ldp, int pm0, int pn0, bool partial = false) {
+          float* __restrict__ P, int ldp, int pm0, int pn0, bool partial = false,
+          HOOK hook = HOOK{}) {
+    static_assert(!HOOK::kActive || (MODE == 0 && ALAY == LAYOUT_MK), "hooks: A [M,K], whole tiles");
     constexpr int BM = BMT, BN = 256, BK = 64;
     constexpr int KC = BK / 8;                 // 16-byte chunks per tile row
     constexpr int ROWS = 64 / KC;              // tile rows per 1 KiB load (8)
@@ -1528,8 +1544,11 @@ quad_body(const u16* __restrict__ A, const u16* __restrict__ B, u16* __restrict_
     const int wm = wave >> 1, wn = wave & 1;
     const int nk = (K + BK - 1) / BK;
 
+    int a_span = M;
+    if constexpr (HOOK::kActive)
+        a_span = hook.a_rows();
     const rsrc4_t ra = AKM ? make_rsrc4(A, span_bytes(K, M, lda))
-                           : make_rsrc4(A, span_bytes(M, K, lda));
+                           : make_rsrc4(A, span_bytes(a_span, K, lda));
     const rsrc4_t rb = KN ? make_rsrc4(B, span_bytes(K, N, ldb))
                           : make_rsrc4(B, span_bytes(N, K, ldb));
 
@@ -1563,6 +1582,10 @@ quad_body(const u16* __restrict__ A, const u16* __restrict__ B, u16* __restrict_
                 const int kr = kn_row(b);
                 const int m = m0 + 8 * ((lane & 31) ^ kn_swz<MF>(kr));
                 a_vo[b] = m < M ? (uint32_t)(kr * lda + m) * 2u - lo : kOutOfRange;
+            } else if constexpr (HOOK::kActive) {
+                const int row = ra < M ? hook.a_row(ra) : -1;
+                a_vo[b] = row >= 0 ? ((uint32_t)row * (uint32_t)lda + (uint32_t)kcol[b & 1]) * 2u - lo
+                                   : kOutOfRange;
             } else {
                 a_vo[b] = ra < M ? (uint32_t)(ra * lda + kcol[b & 1]) * 2u - lo : kOutOfRange;
             }
@@ -1571,7 +1594,13 @@ quad_body(const u16* __restrict__ A, const u16* __restrict__ B, u16* __restrict_
         for (int b = 0; b < NBB; ++b) {
             const int rbn = n0 + rb0 + b * ROWS;
             const uint32_t lo = OFFS ? (uint32_t)(b & 3) * 1024u : 0u;
-            if constexpr (KN) {
+            if constexpr (HOOK::kActive) {
+                const int kr = kn_row(b);
+                const int n = hook.b_row(KN ? 8 * ((lane & 31) ^ kn_swz<MF>(kr)) : rb0 + b * ROWS);
+                b_vo[b] = n < 0 ? kOutOfRange
+                                : (KN ? (uint32_t)kr * (uint32_t)ldb + (uint32_t)n
+                                      : (uint32_t)n * (uint32_t)ldb + (uint32_t)kcol[b & 1]) * 2u - lo;
+            } else if constexpr (KN) {
                 const int kr = kn_row(b);
                 const int n = n0 + 8 * ((lane & 31) ^ kn_swz<MF>(kr));
                 b_vo[b] = n < N ? (uint32_t)(kr * ldb + n) * 2u - lo : kOutOfRange;
@@ -1898,6 +1927,12 @@ quad_body(const u16* __restrict__ A, const u16* __restrict__ B, u16* __restrict_
                 }
             }
         }
+        return;
+    }
+
+    if constexpr (HOOK::kActive) {
+        wait_vm_then_sync<0>();
+        hook.template finish<MF, TM, TN>(acc, lds, wave, lane);
         return;
     }
 
