@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
+#include <stdlib.h>
 
 #include "fused_launch.hpp"
 
@@ -145,6 +146,7 @@ bool tiles_fit(const Layer& l) {
 // that it streams B with (the stream forms read 5.5 TB/s, the tiled ones 4.6 with one row
 // tile per group, the quad kernel 5.1).
 tgemm_fused::Form choose_rows(const Layer& l) {
+    if (const char* e = getenv("TGEMM_FORM")) return (tgemm_fused::Form)(atoi(e) >= 4 && l.b_layout != TGEMM_B_NK ? 2 : atoi(e));
     struct Cost {
         int per_unit;                 // workgroups that share a compute unit
         double alone, shared, fixed;  // us per step in either case; us per launch
@@ -316,6 +318,7 @@ int launch_sum(const Layer& l, const SumArgs& p, hipStream_t s) {
         if (l.groups * cdiv(p.I, 128) * cdiv(p.J, 128) > kMaxDim)
             return TGEMM_ERR_UNSUPPORTED;
         bool large = t256 >= 128, quad = large;
+        if (const char* e = getenv("TGEMM_SUM")) large = atoi(e) != 1, quad = atoi(e) == 0;
         (void)hipGetLastError();
         if (quad && !p.row_index && p.vec && 2 * span(p.rows, p.I, p.ldl) <= kMaxBufferBytes && 2 * span(p.rows, p.J, p.ldr) <= kMaxBufferBytes)
             return status(tgemm_fused::sum_quad(l.dtype, p, s));

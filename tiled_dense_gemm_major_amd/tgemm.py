@@ -7,7 +7,6 @@ fallback: if the library is missing, every call raises.
 from __future__ import annotations
 
 import collections
-import contextlib
 import ctypes
 import os
 
@@ -351,22 +350,23 @@ def gemm(A, B, C=None, b_layout=B_NK, config: Config | None = None, stream=None)
 
 def _matrix(t, what, like=None, shape=None):
     """(address, rows, columns, row stride) of a 2-D tensor, after its checks."""
-    if t.dim() != 2:
-        raise ValueError(f"{what} must have 2 dimensions, not {t.dim()}")
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    size, step = t.shape, t.stride()
+    if len(size) != 2:
+        raise ValueError(f"{what} must have 2 dimensions, not {len(size)}")
+    rows, cols = size
+    if step[1] != 1 and cols > 1:
         raise ValueError(f"{what}: the last dimension must be contiguous")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+    if like is not None and (t.dtype != like.dtype or t.get_device() != like.get_device()):
         raise TypeError(f"{what} must have the dtype and device of the operands "
                         f"({like.dtype}, {like.device}), not {t.dtype}, {t.device}")
-    if shape is not None and (rows, cols) != shape:
+    if shape is not None and size != shape:
         raise ValueError(f"{what} must have shape {shape}, not {(rows, cols)}")
-    return t.data_ptr(), rows, cols, (t.stride(0) if rows > 1 else max(cols, 1))
+    return t.data_ptr(), rows, cols, (step[0] if rows > 1 else max(cols, 1))
 
 
 def _vector(t, what, like, dtype, count):
     """The address of a contiguous tensor of `count` values of `dtype` on like's GPU."""
-    if t.dtype != dtype or t.device != like.device:
+    if t.dtype != dtype or t.get_device() != like.get_device():
         raise TypeError(f"{what} must be {dtype} on {like.device}, not {t.dtype} on {t.device}")
     if t.numel() != count or not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous with {count} elements, not {tuple(t.shape)}")
@@ -382,7 +382,10 @@ def _torch():
     if _torch_names is None:
         import torch
         halves = {torch.float16: F16, torch.bfloat16: BF16}
-        _torch_names = (torch, halves, {**halves, torch.float32: F32})
+        # the address of a GPU's current stream, without making a Stream object of it
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _torch_names = (torch, halves, {**halves, torch.float32: F32}, raw)
     return _torch_names
 
 
@@ -395,18 +398,23 @@ def _operand_dtype(t, what):
     return halves[t.dtype]
 
 
-def _on_device(t):
-    """A context with t's GPU as the current one (kernels launch on the current GPU)."""
-    torch = _torch()[0]
-    if t.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(t.device)
-
-
-def _stream_on(t, stream):
+def _launch(name, t, stream, *args):
+    """The entry point `name` on t's GPU (kernels launch on the current one) and the given or
+    that GPU's current stream."""
+    torch, _, _, raw_stream = _torch()
+    index = t.get_device()
     if stream is None:
-        return _torch()[0].cuda.current_stream(t.device).cuda_stream
-    return stream if isinstance(stream, int) else int(stream.cuda_stream)
+        stream = raw_stream(index)
+    elif not isinstance(stream, int):
+        stream = int(stream.cuda_stream)
+    fn = getattr(load(), name)
+    if index == torch.cuda.current_device():
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, stream)
+    if rc != 0:
+        raise TGemmError(rc, name)
 
 
 def _b_sizes(B, b_layout, k):
@@ -452,9 +460,7 @@ def gemm_fused(A, B, C=None, b_layout=B_NK, bias=None, activation=ACT_NONE, gate
         C = A.new_empty((m, width))
     c, _, _, ldc = _matrix(C, "C", A, (m, width))
     e = _epilogue(A, m, n, width, activation, gated, bias, residual, preact)
-    with _on_device(A):
-        _check(load().gemm_fused(dtype, m, n, k, a, lda, b, ldb, b_layout, c, ldc, e,
-                                 _stream_on(A, stream)), "gemm_fused")
+    _launch("gemm_fused", A, stream, dtype, m, n, k, a, lda, b, ldb, b_layout, c, ldc, e)
     return C
 
 
@@ -489,7 +495,7 @@ def _gradient_buffers(A, rows, n, groups, activation, gated, preact, dZ, product
         wb = backward_workspace_size(rows, n, groups)
         if workspace is None:
             workspace = A.new_empty((max(wb, 16),), dtype=_torch()[0].uint8)
-        elif workspace.device != A.device or not workspace.is_contiguous():
+        elif workspace.get_device() != A.get_device() or not workspace.is_contiguous():
             raise ValueError("the workspace must be contiguous and on the operands' GPU")
         w, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     # the tensors allocated here are kept until the call has been enqueued
@@ -516,11 +522,8 @@ def gemm_fused_backward(dC, A, B, preact=None, b_layout=B_NK, activation=ACT_NON
     z, ldz, d, lddz, w, wb, keep = _gradient_buffers(
         A, m, n, 1, activation, gated, preact, dZ, dA is not None or dB is not None, dbias,
         workspace)
-    with _on_device(A):
-        _check(load().gemm_fused_backward(dtype, m, n, k, dc, lddc, a, lda, b, ldb, b_layout,
-                                          activation, int(bool(gated)), z, ldz, d, lddz, da,
-                                          ldda, db, lddb, dbv, w, wb, _stream_on(A, stream)),
-               "gemm_fused_backward")
+    _launch("gemm_fused_backward", A, stream, dtype, m, n, k, dc, lddc, a, lda, b, ldb, b_layout,
+            activation, int(bool(gated)), z, ldz, d, lddz, da, ldda, db, lddb, dbv, w, wb)
     return dA, dB, dbias
 
 
@@ -530,7 +533,7 @@ def _stack(B, what, like, shape=None):
         raise ValueError(f"{what} must have 3 dimensions, not {B.dim()}")
     if shape is not None and tuple(B.shape) != shape:
         raise ValueError(f"{what} must have shape {shape}, not {tuple(B.shape)}")
-    if B.dtype != like.dtype or B.device != like.device:
+    if B.dtype != like.dtype or B.get_device() != like.get_device():
         raise TypeError(f"{what} must have the dtype and device of the operands "
                         f"({like.dtype}, {like.device}), not {B.dtype}, {B.device}")
     groups, rows, cols = B.shape
@@ -566,10 +569,8 @@ def gemm_grouped(A, B, offsets, C=None, row_index=None, row_div=1, b_layout=B_NK
         C = A.new_empty((rows, width))
     c, _, _, ldc = _matrix(C, "C", A, (rows, width))
     e = _epilogue(A, rows, n, width, activation, gated, bias, residual, preact, groups)
-    with _on_device(A):
-        _check(load().gemm_grouped(dtype, groups, rows, n, k, off, idx, row_div, a, a_rows, lda,
-                                   b, ldb, stride_b, b_layout, c, ldc, e,
-                                   _stream_on(A, stream)), "gemm_grouped")
+    _launch("gemm_grouped", A, stream, dtype, groups, rows, n, k, off, idx, row_div, a, a_rows,
+            lda, b, ldb, stride_b, b_layout, c, ldc, e)
     return C
 
 
@@ -594,11 +595,9 @@ def gemm_grouped_backward(dC, A, B, offsets, preact=None, row_index=None, row_di
     z, ldz, d, lddz, w, wb, keep = _gradient_buffers(
         A, rows, n, groups, activation, gated, preact, dZ, dA is not None or dB is not None,
         dbias, workspace)
-    with _on_device(A):
-        _check(load().gemm_grouped_backward(
-            dtype, groups, rows, n, k, off, idx, row_div, dc, lddc, a, a_rows, lda, b, ldb,
-            stride_b, b_layout, activation, int(bool(gated)), z, ldz, d, lddz, da, ldda, db,
-            lddb, stride_db, dbv, w, wb, _stream_on(A, stream)), "gemm_grouped_backward")
+    _launch("gemm_grouped_backward", A, stream, dtype, groups, rows, n, k, off, idx, row_div, dc,
+            lddc, a, a_rows, lda, b, ldb, stride_b, b_layout, activation, int(bool(gated)), z,
+            ldz, d, lddz, da, ldda, db, lddb, stride_db, dbv, w, wb)
     return dA, dB, dbias
 
 
@@ -627,11 +626,9 @@ def moe_route(logits, k, scoring=SCORE_SOFTMAX, bias=None, groups=1, topk_groups
     i = _vector(ids, "ids", logits, torch.int32, tokens * k)
     w = _vector(weights, "weights", logits, torch.float32, tokens * k)
     bv = 0 if bias is None else _vector(bias, "bias", logits, torch.float32, experts)
-    with _on_device(logits):
-        _check(load().moe_route(dtype, tokens, experts, k, x, ldx, bv, scoring, groups,
-                                groups if topk_groups is None else topk_groups, group_score,
-                                int(bool(renormalize)), scale, i, w,
-                                _stream_on(logits, stream)), "moe_route")
+    _launch("moe_route", logits, stream, dtype, tokens, experts, k, x, ldx, bv, scoring, groups,
+            groups if topk_groups is None else topk_groups, group_score,
+            int(bool(renormalize)), scale, i, w)
     return ids, weights
 
 
@@ -647,10 +644,8 @@ def moe_route_backward(logits, ids, dweights, scoring=SCORE_SOFTMAX, renormalize
     if dlogits is None:
         dlogits = logits.new_empty((tokens, experts))
     dx, _, _, lddx = _matrix(dlogits, "dlogits", logits, (tokens, experts))
-    with _on_device(logits):
-        _check(load().moe_route_backward(dtype, tokens, experts, k, x, ldx, i, dw, scoring,
-                                         int(bool(renormalize)), scale, dx, lddx,
-                                         _stream_on(logits, stream)), "moe_route_backward")
+    _launch("moe_route_backward", logits, stream, dtype, tokens, experts, k, x, ldx, i, dw,
+            scoring, int(bool(renormalize)), scale, dx, lddx)
     return dlogits
 
 
@@ -680,20 +675,17 @@ def moe_plan(ids, experts, offsets=None, order=None, slots=None, workspace=None,
         order = ids.new_empty((count,))
     if slots is None:
         slots = ids.new_empty(ids.shape)
-    need = plan_workspace_size(count, experts)
-    if workspace is None and need:
-        workspace = ids.new_empty((need // 4,))
+    if workspace is None and count > 4096:
+        workspace = ids.new_empty((plan_workspace_size(count, experts) // 4,))
     w = wb = 0
     if workspace is not None:
-        if workspace.device != ids.device or not workspace.is_contiguous():
+        if workspace.get_device() != ids.get_device() or not workspace.is_contiguous():
             raise ValueError("the workspace must be contiguous and on the ids' GPU")
         w, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     off = _vector(offsets, "offsets", ids, torch.int32, experts + 1)
     o = _vector(order, "order", ids, torch.int32, count)
     s = _vector(slots, "slots", ids, torch.int32, count)
-    with _on_device(ids):
-        _check(load().moe_plan(count, experts, i, off, o, s, w, wb, _stream_on(ids, stream)),
-               "moe_plan")
+    _launch("moe_plan", ids, stream, count, experts, i, off, o, s, w, wb)
     return Plan(offsets, order, slots)
 
 
@@ -714,9 +706,7 @@ def moe_combine(O, slots, weights=None, residual=None, Y=None, stream=None):
     y, _, _, ldy = _matrix(Y, "Y", O, (tokens, width))
     r, _, _, ldr = (0, 0, 0, 0) if residual is None else _matrix(residual, "residual", O,
                                                                 (tokens, width))
-    with _on_device(O):
-        _check(load().moe_combine(dtype, tokens, k, width, o, rows, ldo, s, w, r, ldr, y, ldy,
-                                  _stream_on(O, stream)), "moe_combine")
+    _launch("moe_combine", O, stream, dtype, tokens, k, width, o, rows, ldo, s, w, r, ldr, y, ldy)
     return Y
 
 
@@ -737,8 +727,6 @@ def moe_combine_backward(dY, O, slots, weights=None, dO=True, dweights=True, str
     dweights = _gradient(dweights, O, (tokens, k), torch.float32)
     do, _, _, lddo = (0, 0, 0, 0) if dO is None else _matrix(dO, "dO", O, (rows, width))
     dw = 0 if dweights is None else _vector(dweights, "dweights", O, torch.float32, tokens * k)
-    with _on_device(O):
-        _check(load().moe_combine_backward(dtype, tokens, k, width, dy, lddy, o, rows, ldo, s, w,
-                                           do, lddo, dw, _stream_on(O, stream)),
-               "moe_combine_backward")
+    _launch("moe_combine_backward", O, stream, dtype, tokens, k, width, dy, lddy, o, rows, ldo, s,
+            w, do, lddo, dw)
     return dO, dweights
