@@ -6,29 +6,35 @@
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
-#include <stdlib.h>
 
 #include "fused_launch.hpp"
 
 namespace tgemm {
 
-// dbias of group blockIdx.y: the slices' sums in order, four runs of slices side by side.
-__global__ void __launch_bounds__(256) bias_sum(const SlopeArgs p, float* __restrict__ dbias) {
-    __shared__ float red[4][64];
+// dbias of group blockIdx.y: the slices' sums in order, sixteen runs of slices side by side.
+__global__ void __launch_bounds__(1024) bias_sum(const SlopeArgs p, float* __restrict__ dbias) {
+    __shared__ float red[16][64];
     const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
     const int g = (int)blockIdx.y, n = (int)blockIdx.x * 64 + lane;
     int lo, hi;
     group_rows(p, g, lo, hi);
     const int first = slices_before(p, g), count = (hi - lo + kSliceRows - 1) / kSliceRows;
-    const int b = first + wave * count / 4, e = first + (wave + 1) * count / 4;
+    const int b = first + (int)((int64_t)wave * count / 16), e = first + (int)((int64_t)(wave + 1) * count / 16);
     float t = 0.0f;
-    if (n < p.N)
+    if (n < p.N) {
+#pragma unroll 8
         for (int i = b; i < e; ++i)
             t += p.sums[(int64_t)i * p.N + n];
+    }
     red[wave][lane] = t;
     __syncthreads();
-    if (wave == 0 && n < p.N)
-        dbias[(int64_t)g * p.N + n] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+    if (wave == 0 && n < p.N) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 16; ++w)
+            sum += red[w][lane];
+        dbias[(int64_t)g * p.N + n] = sum;
+    }
 }
 
 }  // namespace tgemm
@@ -146,7 +152,6 @@ bool tiles_fit(const Layer& l) {
 // that it streams B with (the stream forms read 5.5 TB/s, the tiled ones 4.6 with one row
 // tile per group, the quad kernel 5.1).
 tgemm_fused::Form choose_rows(const Layer& l) {
-    if (const char* e = getenv("TGEMM_FORM")) return (tgemm_fused::Form)(atoi(e) >= 4 && l.b_layout != TGEMM_B_NK ? 2 : atoi(e));
     struct Cost {
         int per_unit;                 // workgroups that share a compute unit
         double alone, shared, fixed;  // us per step in either case; us per launch
@@ -318,7 +323,6 @@ int launch_sum(const Layer& l, const SumArgs& p, hipStream_t s) {
         if (l.groups * cdiv(p.I, 128) * cdiv(p.J, 128) > kMaxDim)
             return TGEMM_ERR_UNSUPPORTED;
         bool large = t256 >= 128, quad = large;
-        if (const char* e = getenv("TGEMM_SUM")) large = atoi(e) != 1, quad = atoi(e) == 0;
         (void)hipGetLastError();
         if (quad && !p.row_index && p.vec && 2 * span(p.rows, p.I, p.ldl) <= kMaxBufferBytes && 2 * span(p.rows, p.J, p.ldr) <= kMaxBufferBytes)
             return status(tgemm_fused::sum_quad(l.dtype, p, s));
@@ -427,17 +431,26 @@ int backward(const Layer& l, const Gradients& d, void* stream) {
         (void)hipGetLastError();
         if (slices > 0) {
             const dim3 grid((unsigned)slices, (unsigned)columns);
-            if (l.dtype == TGEMM_F16)
-                hipLaunchKernelGGL((tgemm::slope_rows<0>), grid, dim3(256), 0, s, p);
-            else
-                hipLaunchKernelGGL((tgemm::slope_rows<1>), grid, dim3(256), 0, s, p);
+#define SLOPE(DT, G) hipLaunchKernelGGL((tgemm::slope_rows<DT, G>), grid, dim3(256), 0, s, p)
+            if (l.dtype == TGEMM_F16) {
+                if (l.gated)
+                    SLOPE(0, true);
+                else
+                    SLOPE(0, false);
+            } else {
+                if (l.gated)
+                    SLOPE(1, true);
+                else
+                    SLOPE(1, false);
+            }
+#undef SLOPE
             rc = status(hipGetLastError());
             if (rc != TGEMM_OK)
                 return rc;
         }
         if (d.dbias) {
-            hipLaunchKernelGGL(tgemm::bias_sum, dim3((unsigned)cdiv(l.n, 64), (unsigned)l.groups), dim3(256), 0,
-                               s, p, d.dbias);
+            hipLaunchKernelGGL(tgemm::bias_sum, dim3((unsigned)cdiv(l.n, 64), (unsigned)l.groups), dim3(1024),
+                               0, s, p, d.dbias);
             rc = status(hipGetLastError());
             if (rc != TGEMM_OK)
                 return rc;

@@ -192,12 +192,12 @@ __device__ __forceinline__ void activate_slope(int act, float x, float& value, f
         slope = x > 0.0f ? 1.0f : 0.0f;
         break;
     case ACT_GELU: {
+        // Phi(x) = 1/2 +- (1/2 - erfc(|x| / sqrt(2)) / 2); x in the density is kept finite
         float gauss;                       // exp(-x^2 / 2)
-        const float a = fabsf(x);
-        const float half_tail = 0.5f * erfc_pos(0.70710678f * a, gauss);
-        const float phi = x > 0.0f ? 1.0f - half_tail : half_tail;
+        const float tail = erfc_pos(0.70710678f * fabsf(x), gauss);
+        const float phi = 0.5f + copysignf(fmaf(-0.5f, tail, 0.5f), x);
         value = x * phi;
-        slope = phi + (gauss > 0.0f || gauss != gauss ? x * 0.39894228f * gauss : 0.0f);
+        slope = fmaf(__builtin_amdgcn_fmed3f(x, -100.0f, 100.0f) * 0.39894228f, gauss, phi);
         break;
     }
     case ACT_GELU_TANH: {
@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(256) sum_generic(const SumArgs p, int grid_i, 
 // bias_sum, so the result does not depend on the launch order.
 // Bound by memory: 16-byte accesses, each value read and written once.
 // ------------------------------------------------------------------------------------
-constexpr int kSliceRows = 64;
+constexpr int kSliceRows = 16;
 
 struct SlopeArgs {
     const u16* dC;
@@ -578,11 +578,11 @@ __device__ __forceinline__ int slices_before(const SlopeArgs& p, int g) {
     return n;
 }
 
-template <int DT>
+template <int DT, bool GATED>
 __global__ void __launch_bounds__(256) slope_rows(const SlopeArgs p) {
     __shared__ float red[4][2][512];
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int width = p.gated ? p.N >> 1 : p.N;
+    const int width = GATED ? p.N >> 1 : p.N;
     // the slice: group, first row, end row
     int slice = (int)blockIdx.x, lo = 0, hi = 0;
     if (!p.offsets) {
@@ -619,31 +619,43 @@ __global__ void __launch_bounds__(256) slope_rows(const SlopeArgs p) {
     const int n = ((int)blockIdx.y * 64 + lane) * 8, left = width - n;
     float s0[8] = {0, 0, 0, 0, 0, 0, 0, 0}, s1[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     if (left > 0) {
-        for (int r = lo + wave; r < hi; r += 4) {
-            float dy[8], z[8], u[8];
-            load8<DT>(p.dC + (int64_t)r * p.lddc + n, p.vec, left, dy);
-            if (p.Z)
-                load8<DT>(p.Z + (int64_t)r * p.ldz + n, p.vec, left, z);
-            if (p.gated)
-                load8<DT>(p.Z + (int64_t)r * p.ldz + width + n, p.vec, left, u);
+        // a wave's four rows: all loads before the arithmetic
+        constexpr int R = kSliceRows / 4;
+        float dy[R][8], z[R][8], u[GATED ? R : 1][8];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int r = lo + wave * R + i;
+            if (r < hi) {
+                load8<DT>(p.dC + (int64_t)r * p.lddc + n, p.vec, left, dy[i]);
+                if (p.Z)
+                    load8<DT>(p.Z + (int64_t)r * p.ldz + n, p.vec, left, z[i]);
+                if constexpr (GATED)
+                    load8<DT>(p.Z + (int64_t)r * p.ldz + width + n, p.vec, left, u[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int r = lo + wave * R + i;
+            if (r >= hi)
+                break;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 float value = 0.0f, slope = 1.0f;
                 if (p.Z)
-                    activate_slope(p.act, z[e], value, slope);
-                z[e] = dy[e] * slope;
-                if (p.gated) {
-                    z[e] *= u[e];
-                    u[e] = dy[e] * value;
-                    s1[e] += u[e];
+                    activate_slope(p.act, z[i][e], value, slope);
+                z[i][e] = dy[i][e] * slope;
+                if constexpr (GATED) {
+                    z[i][e] *= u[i][e];
+                    u[i][e] = dy[i][e] * value;
+                    s1[e] += u[i][e];
                 }
-                s0[e] += z[e];
+                s0[e] += z[i][e];
             }
             if (p.dZ) {
                 u16* q = p.dZ + (int64_t)r * p.lddz + n;
-                store8<DT>(q, p.vec, left, z);
-                if (p.gated)
-                    store8<DT>(q + width, p.vec, left, u);
+                store8<DT>(q, p.vec, left, z[i]);
+                if constexpr (GATED)
+                    store8<DT>(q + width, p.vec, left, u[i]);
             }
         }
     }
@@ -657,7 +669,7 @@ __global__ void __launch_bounds__(256) slope_rows(const SlopeArgs p) {
     __syncthreads();
     for (int q = tid; q < 1024; q += 256) {
         const int half = q >> 9, c = q & 511, col = (int)blockIdx.y * 512 + c;
-        if (col < width && (half == 0 || p.gated))
+        if (col < width && (half == 0 || GATED))
             p.sums[(int64_t)slice * p.N + half * width + col] =
                 (red[0][half][c] + red[1][half][c]) + (red[2][half][c] + red[3][half][c]);
     }

@@ -25,12 +25,29 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
 // wave's LDS accesses in order, the compiler is kept from moving them.
 __device__ __forceinline__ void wave_lds_sync() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
-// Reductions over the 64 lanes of a wave, the result in every lane.
+// Reductions over the 64 lanes of a wave, the result in every lane.  fp32: four rotations
+// within rows of 16 lanes and two swaps of rows, all in vector registers; fp64 (the rare
+// exact path): shuffles.
+template <int CTRL>
+__device__ __forceinline__ float row_rotate(float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, false));
+}
+template <typename OP>
+__device__ __forceinline__ float wave_all(float v, OP&& op) {
+    v = op(v, row_rotate<0x128>(v));
+    v = op(v, row_rotate<0x124>(v));
+    v = op(v, row_rotate<0x122>(v));
+    v = op(v, row_rotate<0x121>(v));
+    auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2)
-        v = fmaxf(v, __shfl_xor(v, d));
-    return v;
+    return wave_all(v, [](float a, float b) { return fmaxf(a, b); });
+}
+__device__ __forceinline__ float wave_sum(float v) {
+    return wave_all(v, [](float a, float b) { return a + b; });
 }
 __device__ __forceinline__ double wave_max(double v) {
 #pragma unroll
@@ -38,12 +55,32 @@ __device__ __forceinline__ double wave_max(double v) {
         v = fmax(v, __shfl_xor(v, d));
     return v;
 }
-template <typename T>
-__device__ __forceinline__ T wave_sum(T v) {
+__device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
     for (int d = 1; d < 64; d *= 2)
         v += __shfl_xor(v, d);
     return v;
+}
+__device__ __forceinline__ float lane_value(float v, int lane) {
+    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
+}
+// e^x within two units in the last place: 2^(x log2 e) with the rounding of the product
+// carried along.  x above -104 (below, e^x is zero in fp32) and at most 88.
+__device__ __forceinline__ float exp_fine(float x) {
+    x = fmaxf(x, -104.0f);
+    const float h = x * 1.44269504f;
+    float r = fmaf(x, 1.44269504f, -h);
+    r = fmaf(x, 1.92596299e-8f, r);
+    const float e = __builtin_amdgcn_exp2f(h);
+    return fmaf(e, r * 0.693147181f, e);
+}
+__device__ __forceinline__ float logistic_fine(float x) {
+    return __builtin_amdgcn_rcpf(1.0f + exp_fine(fminf(-x, 88.0f)));
+}
+// A float's bits in an order that integers have: for values that are not NaN.
+__device__ __forceinline__ uint32_t ordered(float v) {
+    const uint32_t u = __float_as_uint(v);
+    return u ^ (u >> 31 ? 0xffffffffu : 0x80000000u);
 }
 
 // ------------------------------------------------------------------------------------
@@ -57,10 +94,17 @@ __device__ __forceinline__ T wave_sum(T v) {
 //   the largest finite value.
 //   w = s of the chosen (the bias only selects), divided by the token's sum of them with
 //   `renormalize`, times scale.  Choices past the last candidate: id -1, weight 0.
-// SCORED: c comes from the scores, computed in fp64: in fp32 the scores of unlike logits
-// round to equal values, and which of two near experts is chosen would depend on the
-// order of a sum.  Else everything is fp32 and the choice is exact.
-// ------------------------------------------------------------------------------------
+// SCORED: c comes from the scores.  In fp32 the scores of unlike logits round to equal
+// values, and which of two near experts is chosen would depend on the order of a sum: the
+// choice is made in fp32 where every comparison that it rests on has a margin of several
+// times the scores' error, else the token is done again in fp64.  Not SCORED: the logits
+// themselves are compared, exactly.
+//   The fp32 choice: a search over the lanes' largest values (one ballot per step) finds a
+//   bound that a few more than k values reach; those go to LDS, one per lane, and each
+//   counts the ones before it.  Rounds that take one largest value after the other cost
+//   three times the instructions (52 -> the time in the table of the design notes for
+//   16384 tokens, 256 experts in 8 groups); they remain where more than 64 values reach the
+//   bound (ties), and in fp64.
 struct RouteArgs {
     const void* x;
     const float* bias;
@@ -71,102 +115,21 @@ struct RouteArgs {
     float scale;
 };
 
-template <int DT, int V, bool SCORED>
-__global__ void __launch_bounds__(256) route_tokens(const RouteArgs p) {
-    using T = std::conditional_t<SCORED, double, float>;
-    constexpr float kNone = -__builtin_inff();
-    __shared__ T group_c[SCORED ? 4 : 1][SCORED ? 64 * V : 1];
-    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
-    const int64_t t = (int64_t)blockIdx.x * 4 + wave;
-    if (t >= p.tokens)
-        return;                            // no barrier below: a wave works on its own
-    float x[V];
-    float top = kNone;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int e = lane * V + v;
-        float a = e < p.experts ? load_logit<DT>(p.x, t * p.ldx + e) : kNone;
-        a = a == a ? a : kNone;
-        x[v] = a < __builtin_inff() ? a : 3.402823466e38f;
-        top = fmaxf(top, x[v]);
-    }
-    top = wave_max(top);
-    const float base = top > kNone ? top : 0.0f;
-    T s[V], c[V];
-    T total = 0;
-    if constexpr (SCORED) {
-        if (p.scoring == SCORE_SOFTMAX) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                s[v] = x[v] > kNone ? exp((double)x[v] - (double)base) : 0.0;
-                total += s[v];
-            }
-            total = wave_sum(total);
-            const double inv = total > 0 ? 1.0 / total : 0.0;
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                s[v] *= inv;
-        } else {
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                s[v] = x[v] > kNone ? 1.0 / (1.0 + exp(-(double)x[v])) : 0.0;
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int e = lane * V + v;
-            const double b = p.bias && e < p.experts ? (double)p.bias[e] : 0.0;
-            const double cv = s[v] + b;
-            c[v] = x[v] > kNone && cv == cv ? cv : (double)kNone;
-        }
-        if (p.groups > 1) {
-            // lane g scores group g from the token's values in LDS (a wave's LDS accesses
-            // complete in order), and the best groups are taken one at a time
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                group_c[wave][lane * V + v] = c[v];
-            wave_lds_sync();
-            const int size = p.experts / p.groups;
-            double best = kNone, second = kNone;
-            if (lane < p.groups)
-                for (int i = 0; i < size; ++i) {
-                    const double a = group_c[wave][lane * size + i];
-                    second = a > best ? best : (a > second ? a : second);
-                    best = a > best ? a : best;
-                }
-            if (p.group_score == GROUP_TOP2 && second > kNone)
-                best += second;
-            unsigned long long kept = 0;
-            for (int i = 0; i < p.topk_groups; ++i) {
-                const double m = wave_max(best);
-                if (!(m > kNone))
-                    break;
-                const int g = __builtin_ctzll(__ballot(best == m));
-                kept |= 1ull << g;
-                if (lane == g)
-                    best = kNone;
-            }
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int e = lane * V + v;
-                if (e < p.experts && !((kept >> (e / size)) & 1))
-                    c[v] = kNone;
-            }
-        }
-    } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            c[v] = x[v];
-        if (p.scoring == SCORE_SOFTMAX && !p.renormalize) {
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                total += x[v] > kNone ? expf(x[v] - base) : 0.0f;
-            total = wave_sum(total);
-        }
-    }
-    // the k best: the wave's largest value, its lowest lane, that lane's lowest expert
+// One token's choice: lane i < k gets the i-th id and its selection score's source (the
+// score s, or not SCORED the logit).
+template <typename T>
+struct Choice {
     int id = -1;
-    T w = 0;
-    for (int i = 0; i < p.k; ++i) {
+    T value = 0;
+};
+
+// The exact rounds: the wave's largest value, its lowest lane, that lane's lowest expert.
+// c is used up.
+template <typename T, int V>
+__device__ __forceinline__ Choice<T> choose_in_rounds(T (&c)[V], const T (&s)[V], int k, int lane) {
+    constexpr T kNone = -__builtin_inf();
+    Choice<T> r;
+    for (int i = 0; i < k; ++i) {
         T m = c[0];
 #pragma unroll
         for (int v = 1; v < V; ++v)
@@ -181,33 +144,295 @@ __global__ void __launch_bounds__(256) route_tokens(const RouteArgs p) {
         for (int v = 0; v < V; ++v)
             if (at < 0 && c[v] == best) {
                 at = v;
-                score = SCORED ? s[v] : c[v];
+                score = s[v];
                 if (lane == from)
                     c[v] = kNone;
             }
         const int e = __shfl(lane * V + at, from);
         score = __shfl(score, from);
         if (lane == i) {
-            id = e;
-            w = score;
+            r.id = e;
+            r.value = score;
         }
     }
-    const bool chosen = id >= 0;
-    if constexpr (!SCORED) {
-        // w holds the chosen logit
-        if (p.scoring == SCORE_SIGMOID)
-            w = 1.0f / (1.0f + expf(-w));
-        else
-            w = expf(w - base) / (p.renormalize ? 1.0f : total);
-        w = chosen ? w : 0.0f;
+    return r;
+}
+
+// The best groups, one at a time; lane g holds group g's score.
+__device__ __forceinline__ unsigned long long groups_in_rounds(double score, int topk_groups, int lane) {
+    constexpr double kNone = -__builtin_inf();
+    unsigned long long kept = 0;
+    for (int i = 0; i < topk_groups; ++i) {
+        const double m = wave_max(score);
+        if (!(m > kNone))
+            break;
+        const int g = __builtin_ctzll(__ballot(score == m));
+        kept |= 1ull << g;
+        if (lane == g)
+            score = kNone;
+    }
+    return kept;
+}
+
+// Half the margin that an fp32 comparison of selection values needs, relative to |c| + s:
+// the exponential, the sum over the experts and the division or addition are together
+// within 16 units in the last place (2^-20) for the scores that compete for a choice.
+constexpr float kMargin = 3.8147e-6f;   // 2^-18
+
+template <int DT, int V, bool SCORED>
+__global__ void __launch_bounds__(256) route_tokens(const RouteArgs p) {
+    constexpr float kNone = -__builtin_inff();
+    __shared__ double group_c[SCORED ? 4 : 1][SCORED ? 64 * V : 1];
+    __shared__ float found_c[4][64], found_s[4][64];
+    __shared__ int found_e[4][64];
+    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+    const int64_t t = (int64_t)blockIdx.x * 4 + wave;
+    if (t >= p.tokens)
+        return;                            // no barrier below: a wave works on its own
+    float x[V];
+    float top = kNone;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int e = lane * V + v;
+        float a = e < p.experts ? load_logit<DT>(p.x, t * p.ldx + e) : kNone;
+        a = a == a ? a : kNone;
+        x[v] = (a < __builtin_inff() ? a : 3.402823466e38f) + 0.0f;   // -0 becomes +0
+        top = fmaxf(top, x[v]);
+    }
+    top = wave_max(top);
+    const float base = top > kNone ? top : 0.0f;
+    const bool softmax = p.scoring == SCORE_SOFTMAX;
+
+    // scores and selection values in fp32
+    float s[V], c[V], total = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        s[v] = c[v] = x[v];
+    if (SCORED || (softmax && !p.renormalize)) {
+        // masked logits come out as 0 (softmax) or next to it, and are masked again below
+        float w[V], bias[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e = lane * V + v;
+            bias[v] = SCORED && p.bias ? p.bias[e < p.experts ? e : 0] : 0.0f;
+        }
+        if (softmax) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                w[v] = exp_fine(x[v] - base);
+                total += w[v];
+            }
+            total = wave_sum(total);
+        } else {
+            total = 1.0f;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                w[v] = logistic_fine(x[v]);
+        }
+        if constexpr (SCORED) {
+            const float inv = softmax ? (total > 0.0f ? 1.0f / total : 0.0f) : 1.0f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                s[v] = w[v] * inv;
+                const float cv = s[v] + bias[v];
+                c[v] = x[v] > kNone && cv == cv ? cv : kNone;
+            }
+        }
+    }
+    bool sure = true;                      // every comparison so far had its margin
+    const bool choose_groups = SCORED && p.topk_groups < p.groups;
+    const int size = SCORED ? p.experts / p.groups : 1;
+    // e / size for e below 1024: the product is at least 1 / 2048 away from a whole number
+    const float per_size = 1.0f / (float)size;
+    const auto group_of = [&](int e) { return (int)(((float)e + 0.5f) * per_size); };
+    if (choose_groups) {
+        // lane g scores group g
+        float best = kNone, second = kNone;
+        const int lanes = size / V;
+        if (size % V == 0 && (lanes & (lanes - 1)) == 0) {
+            // a group is `lanes` whole lanes, a power of two: its two largest by shuffles
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                second = fmaxf(second, fminf(best, c[v]));
+                best = fmaxf(best, c[v]);
+            }
+            for (int d = 1; d < lanes; d *= 2) {
+                const float b2 = __shfl_xor(best, d), s2 = __shfl_xor(second, d);
+                second = fmaxf(fmaxf(second, s2), fminf(best, b2));
+                best = fmaxf(best, b2);
+            }
+            best = __shfl(best, lane * lanes < 64 ? lane * lanes : 0);
+            second = __shfl(second, lane * lanes < 64 ? lane * lanes : 0);
+        } else {
+            float* row = reinterpret_cast<float*>(group_c[wave]);
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                row[lane * V + v] = c[v];
+            wave_lds_sync();
+            if (lane < p.groups)
+                for (int i = 0; i < size; ++i) {
+                    const float a = row[lane * size + i];
+                    second = fmaxf(second, fminf(best, a));
+                    best = fmaxf(best, a);
+                }
+            wave_lds_sync();
+        }
+        float score = lane < p.groups ? best : kNone;
+        if (p.group_score == GROUP_TOP2 && second > kNone)
+            score += second;
+        score = lane < p.groups ? score : kNone;
+        // a group's place: the groups before it
+        int place = 0;
+        for (int g = 0; g < p.groups; ++g) {
+            const float o = lane_value(score, g);
+            place += o > score || (o == score && g < lane);
+        }
+        const bool keep = lane < p.groups && place < p.topk_groups && score > kNone;
+        const unsigned long long kept = __ballot(keep);
+        // the last group kept and the first one left need a margin between them
+        const unsigned long long in = __ballot(lane < p.groups && place == p.topk_groups - 1);
+        const unsigned long long out = __ballot(lane < p.groups && place == p.topk_groups);
+        const float a = lane_value(score, __builtin_ctzll(in)), b = lane_value(score, __builtin_ctzll(out));
+        sure = !(a > kNone) || !(b > kNone) || a - b > 4.0f * kMargin * (fabsf(a) + 2.0f);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e = lane * V + v;
+            if (e < p.experts && !((kept >> group_of(e)) & 1))
+                c[v] = kNone;
+        }
+    }
+
+    Choice<float> got;
+    bool placed = false;
+    if (sure) {
+        // the largest bound that more than k lanes' largest values reach (all valid ones, if
+        // there are fewer), to 16 bits
+        float m = c[0];
+#pragma unroll
+        for (int v = 1; v < V; ++v)
+            m = fmaxf(m, c[v]);
+        const uint32_t key = ordered(m);
+        uint32_t bound = 0;
+#pragma unroll
+        for (int bit = 31; bit >= 16; --bit) {
+            const uint32_t tryit = bound | (1u << bit);
+            if (__popcll(__ballot(key >= tryit)) > p.k)
+                bound = tryit;
+        }
+        const uint32_t low = ordered(kNone);
+        bound = bound > low ? bound : low + 1;
+        // their places in LDS follow the experts' order: those of the lanes before, then the
+        // lane's own
+        int n = 0, at = 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const unsigned long long mask = __ballot(ordered(c[v]) >= bound);
+            at = __builtin_amdgcn_mbcnt_lo((uint32_t)mask, at);
+            at = __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), at);
+            n += __popcll(mask);
+        }
+        if (n <= 64) {
+            placed = true;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (ordered(c[v]) >= bound) {
+                    found_c[wave][at] = c[v];
+                    found_s[wave][at] = s[v];
+                    found_e[wave][at] = lane * V + v;
+                    ++at;
+                }
+            wave_lds_sync();
+            const bool mine = lane < n;
+            const float fc = mine ? found_c[wave][lane] : kNone, fs = mine ? found_s[wave][lane] : 0.0f;
+            const int fe = mine ? found_e[wave][lane] : -1;
+            int place = 0;
+#pragma unroll 4
+            for (int i = 0; i < n; ++i) {
+                const float o = lane_value(fc, i);
+                place += i < lane ? o >= fc : o > fc;
+            }
+            wave_lds_sync();
+            if (mine) {
+                found_c[wave][place] = fc;
+                found_s[wave][place] = fs;
+                found_e[wave][place] = fe;
+            }
+            wave_lds_sync();
+            if (lane < n && lane < p.k) {
+                got.id = found_e[wave][lane];
+                got.value = found_s[wave][lane];
+            }
+            if constexpr (SCORED) {
+                bool near = false;
+                if (lane < p.k && lane + 1 < n) {
+                    const float a = found_c[wave][lane], b = found_c[wave][lane + 1];
+                    const float scale = fabsf(a) + found_s[wave][lane] + found_s[wave][lane + 1];
+                    near = !(a - b > 2.0f * kMargin * scale);
+                }
+                sure = __ballot(near) == 0;
+            }
+        }
+    }
+    float w;
+    if constexpr (SCORED) {
+        if (!sure || !placed) {
+            // the token in fp64
+            double s64[V], c64[V], sum = 0;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                s64[v] = x[v] > kNone ? (softmax ? exp((double)x[v] - (double)base) : 1.0 / (1.0 + exp(-(double)x[v])))
+                                      : 0.0;
+                sum += s64[v];
+            }
+            sum = softmax ? wave_sum(sum) : 1.0;
+            const double inv = sum > 0 ? 1.0 / sum : 0.0;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int e = lane * V + v;
+                s64[v] *= inv;
+                const double cv = s64[v] + (p.bias && e < p.experts ? (double)p.bias[e] : 0.0);
+                c64[v] = x[v] > kNone && cv == cv ? cv : -__builtin_inf();
+            }
+            if (choose_groups) {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    group_c[wave][lane * V + v] = c64[v];
+                wave_lds_sync();
+                double best = -__builtin_inf(), second = best;
+                if (lane < p.groups)
+                    for (int i = 0; i < size; ++i) {
+                        const double a = group_c[wave][lane * size + i];
+                        second = a > best ? best : (a > second ? a : second);
+                        best = a > best ? a : best;
+                    }
+                if (p.group_score == GROUP_TOP2 && second > -__builtin_inf())
+                    best += second;
+                const unsigned long long kept = groups_in_rounds(best, p.topk_groups, lane);
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const int e = lane * V + v;
+                    if (e < p.experts && !((kept >> group_of(e)) & 1))
+                        c64[v] = -__builtin_inf();
+                }
+            }
+            const Choice<double> exact = choose_in_rounds<double, V>(c64, s64, p.k, lane);
+            got.id = exact.id;
+            got.value = (float)exact.value;
+        }
+        w = got.id >= 0 ? got.value : 0.0f;
+    } else {
+        if (!placed)
+            got = choose_in_rounds<float, V>(c, s, p.k, lane);
+        w = softmax ? exp_fine(got.value - base) / (p.renormalize ? 1.0f : total) : logistic_fine(got.value);
+        w = got.id >= 0 ? w : 0.0f;
     }
     if (p.renormalize) {
-        const T sum = wave_sum(w);
-        w = sum > 0 ? w / sum : w;
+        const float sum = wave_sum(w);
+        w = sum > 0.0f ? w / sum : w;
     }
     if (lane < p.k) {
-        p.ids[t * p.k + lane] = id;
-        p.weights[t * p.k + lane] = (float)(w * (T)p.scale);
+        p.ids[t * p.k + lane] = got.id;
+        p.weights[t * p.k + lane] = w * p.scale;
     }
 }
 
@@ -268,7 +493,7 @@ __global__ void __launch_bounds__(256) route_grad(const RouteGradArgs p) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         if (x[v] > kNone)
-            s[v] = p.scoring == SCORE_SOFTMAX ? expf(x[v] - base) : 1.0f / (1.0f + expf(-x[v]));
+            s[v] = p.scoring == SCORE_SOFTMAX ? exp_fine(x[v] - base) : logistic_fine(x[v]);
         else
             s[v] = 0.0f;
         total += p.renormalize ? (mine[v] ? s[v] : 0.0f) : s[v];
@@ -290,7 +515,7 @@ __global__ void __launch_bounds__(256) route_grad(const RouteGradArgs p) {
         if (mine[v] || (p.scoring == SCORE_SOFTMAX && !p.renormalize))
             d = s[v] * inv * (g[v] - dot);
         if (p.scoring == SCORE_SIGMOID)
-            d *= 1.0f / (1.0f + expf(x[v]));       // 1 - s
+            d *= logistic_fine(-x[v]);       // 1 - s
         if constexpr (DT == DT_F32)
             static_cast<float*>(p.dx)[t * p.lddx + e] = d;
         else
@@ -391,6 +616,7 @@ __global__ void __launch_bounds__(kPlanWaves * 64) plan_place(const PlanArgs p) 
         all = here;
         if (p.chunks > 1) {
             all = 0;
+#pragma unroll 8
             for (int b = 0; b < p.chunks; ++b) {
                 const int c = p.counts[(int64_t)b * p.experts + tid];
                 before += b < (int)blockIdx.x ? c : 0;
