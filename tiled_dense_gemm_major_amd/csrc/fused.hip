@@ -158,8 +158,9 @@ tgemm_fused::Form choose_rows(const Layer& l) {
         double rate;                  // TB/s
     };
     static const Cost kCost[tgemm_fused::FORMS] = {
-        {1, 1.34, 1.34, 9, 5.1}, {2, 0.62, 0.97, 6, 4.6}, {2, 0.39, 0.61, 5, 4.6}, {3, 0.26, 0.45, 5, 4.6},
-        {2, 0.16, 0.30, 4, 5.5}, {4, 0.22, 0.55, 4, 5.6}, {2, 0.18, 0.32, 4, 5.4}, {1, 0.24, 0.24, 4, 5.0}};
+        {1, 1.34, 1.34, 9, 5.1}, {2, 0.80, 0.97, 6, 4.6}, {1, 0.60, 0.60, 6, 4.6}, {2, 0.39, 0.68, 5, 4.6},
+        {3, 0.26, 0.45, 5, 4.6}, {1, 0.24, 0.24, 5, 4.6}, {2, 0.16, 0.30, 4, 5.5}, {4, 0.22, 0.55, 4, 5.6},
+        {2, 0.18, 0.32, 4, 5.4}, {1, 0.24, 0.24, 4, 5.0}};
     // groups that have rows, if each row fell into any group alike
     const double live = l.groups == 1 ? 1.0 : l.groups * (1.0 - exp(-(double)l.rows / l.groups));
     const double avg = l.rows / live, steps = (double)cdiv(l.k, 64);
@@ -167,8 +168,8 @@ tgemm_fused::Form choose_rows(const Layer& l) {
     int best = 1;
     double least = 0;
     for (int f = 0; f < tgemm_fused::FORMS; ++f) {
-        if (f >= tgemm_fused::FORM_STREAM16 && l.b_layout != TGEMM_B_NK)
-            break;
+        if (!tgemm_fused::form_takes((tgemm_fused::Form)f, l.b_layout))
+            continue;
         const Cost& c = kCost[f];
         const tgemm_fused::Tile t = tgemm_fused::kTiles[f];
         const double row_tiles = l.groups == 1 ? (double)cdiv(l.rows, t.m)
@@ -196,7 +197,7 @@ int launch_rows(const Layer& l, const FusedArgs& p, hipStream_t s) {
             return TGEMM_ERR_UNSUPPORTED;
         (void)hipGetLastError();
         if (form >= tgemm_fused::FORM_STREAM16)
-            return status(tgemm_fused::rows_stream(l.dtype, form, p, tm, (int)tn, s));
+            return status(tgemm_fused::rows_stream(l.dtype, l.b_layout, form, p, tm, (int)tn, s));
         if (form == tgemm_fused::FORM_QUAD)
             return status(tgemm_fused::rows_quad(l.dtype, l.b_layout, p, tm, (int)tn, s));
         return status(l.b_layout == TGEMM_B_NK ? tgemm_fused::rows_tiled_nk(l.dtype, form, p, tm, (int)tn, s)
@@ -313,20 +314,47 @@ struct Gradients {
     int64_t workspace_bytes;
 };
 
+// The form of a sum over rows, by the same estimate: rounds of workgroups times steps of 64
+// rows times the time of a step.
+tgemm_fused::SumForm choose_sum(const Layer& l, const SumArgs& p, bool quad) {
+    struct Cost {
+        int per_unit;
+        double alone, shared, fixed;
+    };
+    static const Cost kCost[tgemm_fused::SUM_FORMS] = {
+        {1, 1.43, 1.43, 8}, {1, 1.75, 1.75, 9}, {2, 0.72, 1.05, 6}, {2, 0.5, 0.55, 5}};
+    const double steps = (double)cdiv(cdiv(l.rows, l.groups), 64);
+    int best = 1;
+    double least = 0;
+    for (int f = quad ? 0 : 1; f < tgemm_fused::SUM_FORMS; ++f) {
+        const int t = tgemm_fused::kSumTiles[f];
+        const double tiles = (double)(l.groups * cdiv(p.I, t) * cdiv(p.J, t));
+        const Cost& c = kCost[f];
+        const double slots = 256.0 * c.per_unit, full = floor(tiles / slots), rest = tiles - full * slots;
+        const double cost = steps * (full * c.shared + (rest > 256 ? c.shared : (rest > 0 ? c.alone : 0))) +
+                            c.fixed * (full + (rest > 0));
+        if (f == (quad ? 0 : 1) || cost < least) {
+            best = f;
+            least = cost;
+        }
+    }
+    return (tgemm_fused::SumForm)best;
+}
+
 int launch_sum(const Layer& l, const SumArgs& p, hipStream_t s) {
     const auto through = [&](bool indexed, int64_t cols, int64_t ld) {
         return ld <= (int64_t(1) << 23) && cols % 8 == 0 && ld % 8 == 0 &&
                (!indexed || 2 * span(p.a_rows, cols, ld) <= kMaxBufferBytes);
     };
     if (al16(p.left) && al16(p.right) && through(p.index_left, p.I, p.ldl) && through(p.index_right, p.J, p.ldr)) {
-        const int64_t t256 = l.groups * cdiv(p.I, 256) * cdiv(p.J, 256);
-        if (l.groups * cdiv(p.I, 128) * cdiv(p.J, 128) > kMaxDim)
+        if (l.groups * cdiv(p.I, 64) * cdiv(p.J, 64) > kMaxDim)
             return TGEMM_ERR_UNSUPPORTED;
-        bool large = t256 >= 128, quad = large;
+        const bool quad = !p.row_index && p.vec && 2 * span(p.rows, p.I, p.ldl) <= kMaxBufferBytes &&
+                          2 * span(p.rows, p.J, p.ldr) <= kMaxBufferBytes;
+        const tgemm_fused::SumForm form = choose_sum(l, p, quad);
         (void)hipGetLastError();
-        if (quad && !p.row_index && p.vec && 2 * span(p.rows, p.I, p.ldl) <= kMaxBufferBytes && 2 * span(p.rows, p.J, p.ldr) <= kMaxBufferBytes)
-            return status(tgemm_fused::sum_quad(l.dtype, p, s));
-        return status(tgemm_fused::sum_tiled(l.dtype, large, p, s));
+        return status(form == tgemm_fused::SUM_QUAD ? tgemm_fused::sum_quad(l.dtype, p, s)
+                                                    : tgemm_fused::sum_tiled(l.dtype, form, p, s));
     }
     const int64_t gi = cdiv(p.I, 64), gj = cdiv(p.J, 64);
     if (l.groups * gi * gj > kMaxDim)

@@ -238,15 +238,19 @@ __device__ __forceinline__ void unpack8(u32x4 v, float (&x)[8]) {
         x[e] = to_float<DT>(h[e]);
 }
 
+__device__ __forceinline__ u32x4 load8_raw(const u16* p, bool vec, int left) {
+    if (vec && left >= 8)
+        return *reinterpret_cast<const u32x4*>(p);
+    u16x8 h;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        h[e] = e < left ? p[e] : (u16)0;
+    return __builtin_bit_cast(u32x4, h);
+}
+
 template <int DT>
 __device__ __forceinline__ void load8(const u16* p, bool vec, int left, float (&x)[8]) {
-    if (vec && left >= 8) {
-        unpack8<DT>(*reinterpret_cast<const u32x4*>(p), x);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            x[e] = e < left ? to_float<DT>(p[e]) : 0.0f;
-    }
+    unpack8<DT>(load8_raw(p, vec, left), x);
 }
 
 template <int DT>
@@ -580,7 +584,7 @@ __device__ __forceinline__ int slices_before(const SlopeArgs& p, int g) {
 
 template <int DT, bool GATED>
 __global__ void __launch_bounds__(256) slope_rows(const SlopeArgs p) {
-    __shared__ float red[4][2][512];
+    __shared__ __attribute__((aligned(16))) float red[4][GATED ? 2 : 1][512];
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int width = GATED ? p.N >> 1 : p.N;
     // the slice: group, first row, end row
@@ -621,16 +625,16 @@ __global__ void __launch_bounds__(256) slope_rows(const SlopeArgs p) {
     if (left > 0) {
         // a wave's four rows: all loads before the arithmetic
         constexpr int R = kSliceRows / 4;
-        float dy[R][8], z[R][8], u[GATED ? R : 1][8];
+        u32x4 dy_raw[R], z_raw[R], u_raw[R];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const int r = lo + wave * R + i;
             if (r < hi) {
-                load8<DT>(p.dC + (int64_t)r * p.lddc + n, p.vec, left, dy[i]);
+                dy_raw[i] = load8_raw(p.dC + (int64_t)r * p.lddc + n, p.vec, left);
                 if (p.Z)
-                    load8<DT>(p.Z + (int64_t)r * p.ldz + n, p.vec, left, z[i]);
+                    z_raw[i] = load8_raw(p.Z + (int64_t)r * p.ldz + n, p.vec, left);
                 if constexpr (GATED)
-                    load8<DT>(p.Z + (int64_t)r * p.ldz + width + n, p.vec, left, u[i]);
+                    u_raw[i] = load8_raw(p.Z + (int64_t)r * p.ldz + width + n, p.vec, left);
             }
         }
 #pragma unroll
@@ -638,24 +642,30 @@ __global__ void __launch_bounds__(256) slope_rows(const SlopeArgs p) {
             const int r = lo + wave * R + i;
             if (r >= hi)
                 break;
+            float dy[8], z[8], u[8];
+            unpack8<DT>(dy_raw[i], dy);
+            if (p.Z)
+                unpack8<DT>(z_raw[i], z);
+            if constexpr (GATED)
+                unpack8<DT>(u_raw[i], u);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 float value = 0.0f, slope = 1.0f;
                 if (p.Z)
-                    activate_slope(p.act, z[i][e], value, slope);
-                z[i][e] = dy[i][e] * slope;
+                    activate_slope(p.act, z[e], value, slope);
+                z[e] = dy[e] * slope;
                 if constexpr (GATED) {
-                    z[i][e] *= u[i][e];
-                    u[i][e] = dy[i][e] * value;
-                    s1[e] += u[i][e];
+                    z[e] *= u[e];
+                    u[e] = dy[e] * value;
+                    s1[e] += u[e];
                 }
-                s0[e] += z[i][e];
+                s0[e] += z[e];
             }
             if (p.dZ) {
                 u16* q = p.dZ + (int64_t)r * p.lddz + n;
-                store8<DT>(q, p.vec, left, z[i]);
+                store8<DT>(q, p.vec, left, z);
                 if constexpr (GATED)
-                    store8<DT>(q + width, p.vec, left, u[i]);
+                    store8<DT>(q + width, p.vec, left, u);
             }
         }
     }
@@ -664,12 +674,13 @@ __global__ void __launch_bounds__(256) slope_rows(const SlopeArgs p) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         red[wave][0][lane * 8 + e] = s0[e];
-        red[wave][1][lane * 8 + e] = s1[e];
+        if constexpr (GATED)
+            red[wave][1][lane * 8 + e] = s1[e];
     }
     __syncthreads();
-    for (int q = tid; q < 1024; q += 256) {
+    for (int q = tid; q < (GATED ? 1024 : 512); q += 256) {
         const int half = q >> 9, c = q & 511, col = (int)blockIdx.y * 512 + c;
-        if (col < width && (half == 0 || GATED))
+        if (col < width)
             p.sums[(int64_t)slice * p.N + half * width + col] =
                 (red[0][half][c] + red[1][half][c]) + (red[2][half][c] + red[3][half][c]);
     }

@@ -4,7 +4,7 @@
 
 namespace tgemm_fused {
 
-hipError_t sum_tiled(int dtype, bool large, const SumArgs& p, hipStream_t s) {
+hipError_t sum_tiled(int dtype, SumForm form, const SumArgs& p, hipStream_t s) {
 #define SUM(DT, BI, BJ, WI, WJ, ST, OCC)                                                   \
     do {                                                                                   \
         const int gi = (p.I + BI - 1) / BI, gj = (p.J + BJ - 1) / BJ;                      \
@@ -18,10 +18,11 @@ hipError_t sum_tiled(int dtype, bool large, const SumArgs& p, hipStream_t s) {
         else                                                                               \
             SUM(1, BI, BJ, WI, WJ, ST, OCC);                                               \
     } while (0)
-    if (large)
-        FORM(256, 256, 2, 4, 2, 2);
-    else
-        FORM(128, 128, 2, 2, 2, 2);
+    switch (form) {
+    case SUM_128: FORM(128, 128, 2, 2, 2, 2); break;
+    case SUM_SMALL: FORM(64, 64, 2, 1, 4, 2); break;
+    default: FORM(256, 256, 2, 4, 2, 2); break;
+    }
 #undef FORM
 #undef SUM
     return hipGetLastError();

@@ -135,9 +135,14 @@ __device__ __forceinline__ void rows_epilogue(const FusedArgs& p, int g, float* 
 // ------------------------------------------------------------------------------------
 // The tiled kernel over rows of groups: A rows [M,K] (through the row index, if any), B
 // [N,K] or [K,N].  WM x WN waves of (BM/WM) x (BN/WN), MFMA 32x32x16, ST stages.
-//   Step t waits until its tile has landed (the loads of up to ST-2 later tiles stay in
-//   flight) and meets the other waves, which have then also read all of tile t-1; sends
-//   the loads of tile t+ST-1 into the stage that tile left; and computes tile t.
+//   A step's four sub-steps of 16 k run the MFMAs of operands read one sub-step before; in
+//   the last, after half of its MFMAs, each wave waits until its loads of tile t+1 have
+//   landed (those of up to ST-2 later tiles stay in flight) and meets the others, which
+//   have then also read all of tile t; the loads of tile t+ST go into the stage that tile
+//   leaves, and the first operands of tile t+1 are read beside the other half.  (Reading a
+//   sub-step's operands right before its MFMAs leaves the matrix cores waiting for the LDS
+//   half of the time where a SIMD holds one wave: 1300 cycles a step of 128 x 128 x 64
+//   instead of the 512 of its MFMAs; more stages do not help.)
 //   Loads past the last tile read nothing (zeros), so that every step has the same number
 //   of loads in flight.
 // ------------------------------------------------------------------------------------
@@ -222,36 +227,57 @@ fused_tiled(const FusedArgs p, int grid_n, int group_m) {
         for (int j = 0; j < TN; ++j)
             kb[j] = kc_at<BN>(lane, wn * WTN, j);
     }
-#pragma unroll
-    for (int t = 0; t < ST - 1; ++t)
-        load(t, t);
-    int slot = 0;
-    for (int t = 0; t < nk; ++t) {
-        wait_vm_then_sync<(ST - 2) * LOADS>();
-        load(t + ST - 1, slot == 0 ? ST - 1 : slot - 1);
+    u32x4 fa[2][TM], fb[2][TN];
+    auto read = [&](int slot, int s, auto bufc) {       // the operands of sub-step s
+        constexpr int buf = decltype(bufc)::value;
         const u16* as = lds + slot * STAGE + (wm * WTM + lr) * kTileK;
         const u16* bs = lds + slot * STAGE + SLOT_A;
+        const int ko = (((2 * s) | half) ^ xr) * 8;
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const int ko = (((2 * s) | half) ^ xr) * 8;
-            u32x4 fa[TM], fb[TN];
-#pragma unroll
-            for (int j = 0; j < TN; ++j) {
-                if constexpr (LAYOUT == LAYOUT_NK)
-                    fb[j] = *reinterpret_cast<const u32x4*>(bs + (wn * WTN + 32 * j + lr) * kTileK + ko);
-                else
-                    fb[j] = read_kcols<BN>(bs + kb[j] + 16 * s * BN);
-            }
-#pragma unroll
-            for (int i = 0; i < TM; ++i)
-                fa[i] = *reinterpret_cast<const u32x4*>(as + 32 * i * kTileK + ko);
-#pragma unroll
-            for (int i = 0; i < TM; ++i)
-#pragma unroll
-                for (int j = 0; j < TN; ++j)
-                    acc[i][j] = mfma_32x32x16<DT>(fb[j], fa[i], acc[i][j]);
+        for (int j = 0; j < TN; ++j) {
+            if constexpr (LAYOUT == LAYOUT_NK)
+                fb[buf][j] = *reinterpret_cast<const u32x4*>(bs + (wn * WTN + 32 * j + lr) * kTileK + ko);
+            else
+                fb[buf][j] = read_kcols<BN>(bs + kb[j] + 16 * s * BN);
         }
-        slot = slot + 1 == ST ? 0 : slot + 1;
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+            fa[buf][i] = *reinterpret_cast<const u32x4*>(as + 32 * i * kTileK + ko);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto multiply = [&](auto bufc, auto fromc, auto toc) {   // blocks [from, to) of the wave's
+        constexpr int buf = decltype(bufc)::value;
+        static_for<decltype(fromc)::value, decltype(toc)::value>([&](auto jc) {
+            constexpr int i = decltype(jc)::value / TN, j = decltype(jc)::value % TN;
+            acc[i][j] = mfma_32x32x16<DT>(fb[buf][j], fa[buf][i], acc[i][j]);
+        });
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
+    using IH = std::integral_constant<int, TM * TN / 2>;
+    using IE = std::integral_constant<int, TM * TN>;
+#pragma unroll
+    for (int t = 0; t < ST; ++t)
+        load(t, t);
+    wait_vm_then_sync<(ST - 1) * LOADS>();
+    read(0, 0, I0{});
+    int slot = 0;
+    for (int t = 0; t < nk; ++t) {
+        const int next = slot + 1 == ST ? 0 : slot + 1;
+        read(slot, 1, I1{});
+        multiply(I0{}, I0{}, IE{});
+        read(slot, 2, I0{});
+        multiply(I1{}, I0{}, IE{});
+        read(slot, 3, I1{});
+        multiply(I0{}, I0{}, IE{});
+        multiply(I1{}, I0{}, IH{});
+        wait_vm_then_sync<(ST - 2) * LOADS>();
+        __builtin_amdgcn_sched_barrier(0);
+        load(t + ST, slot);
+        read(next, 0, I0{});
+        multiply(I1{}, IH{}, IE{});
+        slot = next;
     }
     wait_vm_then_sync<0>();            // no load writes LDS any more, no wave reads it
 
@@ -338,8 +364,9 @@ sum_quad(const SumArgs p, int grid_i, int grid_j) {
 // ------------------------------------------------------------------------------------
 // The tiled kernel of the sums over a group's rows (sum_generic's products): both operands
 // have the summed row as their row index, so both are KCols tiles, read by transposing
-// reads.  An operand that goes through the row index has each tile's 64 indices fetched by
-// a direct-to-LDS load of its own, one tile ahead of the tile that needs them.
+// reads.  With a row index, each tile's 64 indices come by a direct-to-LDS load of their own
+// into a ring of four, four tiles before the tile whose loads need them (so that they are
+// there by the wait for an older tile).
 // ------------------------------------------------------------------------------------
 __device__ __forceinline__ void dma4_at(rsrc4_t r, uint32_t lds_byte, uint32_t voff) {
     const uint32_t m0v = __builtin_amdgcn_readfirstlane(lds_byte);
@@ -357,7 +384,7 @@ sum_tiled(const SumArgs p, int grid_i, int grid_j) {
     constexpr int SRS = WTJ + 8;                        // staged row in elements
     static_assert(NW * 32 * SRS <= ST * STAGE, "D staging fits the ring");
     __shared__ __attribute__((aligned(1024))) u16 lds[ST * STAGE];
-    __shared__ __attribute__((aligned(256))) int32_t idx[NW][2][64];
+    __shared__ __attribute__((aligned(256))) int32_t idx[NW][4][64];
     const int per = grid_i * grid_j, g = (int)blockIdx.x / per;
     int ti, tj, lo, hi;
     tile_of((int)blockIdx.x % per, grid_i, grid_j, 4, ti, tj);
@@ -377,7 +404,7 @@ sum_tiled(const SumArgs p, int grid_i, int grid_j) {
     const rsrc4_t rx = make_rsrc4(p.row_index + (indexed ? lo : 0), indexed ? (uint32_t)K * 4u : 0u);
     auto load_idx = [&](int t) {
         if (indexed)
-            dma4_at(rx, idx0 + (uint32_t)((t & 1) * 256), (uint32_t)(t * kTileK + lane) * 4u);
+            dma4_at(rx, idx0 + (uint32_t)((t & 3) * 256), (uint32_t)(t * kTileK + lane) * 4u);
     };
     auto load = [&](int t, int slot) {
         const int k0 = t * kTileK;
@@ -395,7 +422,7 @@ sum_tiled(const SumArgs p, int grid_i, int grid_j) {
                 int row = kk;
                 bool ok = n < limit && kk < rows;
                 if (via) {
-                    const int v = idx[wave][t & 1][kk];
+                    const int v = idx[wave][t & 3][kk];
                     row = p.row_div == 1 ? v : v / p.row_div;
                     ok = ok && v >= 0 && row < p.a_rows;
                 }
@@ -421,55 +448,73 @@ sum_tiled(const SumArgs p, int grid_i, int grid_j) {
     for (int j = 0; j < TJ; ++j)
         ra[j] = kc_at<BJ>(lane, wj * WTJ, j);
     // a wave reads the indices that it loaded itself: its own wait is enough
-    load_idx(0);
-    load_idx(1);
-    wait_vm<0>();
-    if (nk > 0) {
 #pragma unroll
-        for (int t = 0; t < ST - 1; ++t) {
-            load(t, t);
-            wave_lds_order();          // the indices of tile t are read
-            load_idx(t + 2);
-            if (indexed)
-                wait_vm<0>();
-        }
-    }
-    int slot = 0;
-    for (int t = 0; t < nk; ++t) {
-        // in flight past this point: the tiles t+1 .. t+ST-2 and, indexed, the indices that
-        // were sent after tile t+ST-2 (so that waiting for tile t+ST-2's would be needed
-        // only if they were older: loads complete in order)
-        if constexpr (ST == 2) {
-            wait_vm_then_sync<0>();
-        } else {
-            if (indexed)
-                wait_vm_then_sync<0>();
-            else
-                wait_vm_then_sync<(ST - 2) * LOADS>();
-        }
-        load(t + ST - 1, slot == 0 ? ST - 1 : slot - 1);
+    for (int t = 0; t < 4; ++t)
+        load_idx(t);
+    wait_vm<0>();
+    const auto send = [&](int t, int slot) {      // tile t, and the indices of tile t + 4
+        load(t, slot);
         if (indexed) {
-            wave_lds_order();
-            load_idx(t + ST + 1);
+            wave_lds_order();                     // the indices of tile t are read
+            load_idx(t + 4);
         }
+    };
+    u32x4 fl[2][TI], fr[2][TJ];
+    auto read = [&](int slot, int s, auto bufc) {
+        constexpr int buf = decltype(bufc)::value;
         const u16* ls = lds + slot * STAGE;
         const u16* rs = ls + SLOT_L;
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            u32x4 fl[TI], fr[TJ];
+        for (int j = 0; j < TJ; ++j)
+            fr[buf][j] = read_kcols<BJ>(rs + ra[j] + 16 * s * BJ);
 #pragma unroll
-            for (int j = 0; j < TJ; ++j)
-                fr[j] = read_kcols<BJ>(rs + ra[j] + 16 * s * BJ);
+        for (int i = 0; i < TI; ++i)
+            fl[buf][i] = read_kcols<BI>(ls + la[i] + 16 * s * BI);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto multiply = [&](auto bufc, auto fromc, auto toc) {
+        constexpr int buf = decltype(bufc)::value;
+        static_for<decltype(fromc)::value, decltype(toc)::value>([&](auto jc) {
+            constexpr int i = decltype(jc)::value / TJ, j = decltype(jc)::value % TJ;
+            acc[i][j] = mfma_32x32x16<DT>(fr[buf][j], fl[buf][i], acc[i][j]);
+        });
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
+    using IH = std::integral_constant<int, TI * TJ / 2>;
+    using IE = std::integral_constant<int, TI * TJ>;
+    static_assert(ST <= 4, "the indices of the first tiles are there, and at most three later tiles in flight");
 #pragma unroll
-            for (int i = 0; i < TI; ++i)
-                fl[i] = read_kcols<BI>(ls + la[i] + 16 * s * BI);
-#pragma unroll
-            for (int i = 0; i < TI; ++i)
-#pragma unroll
-                for (int j = 0; j < TJ; ++j)
-                    acc[i][j] = mfma_32x32x16<DT>(fr[j], fl[i], acc[i][j]);
-        }
-        slot = slot + 1 == ST ? 0 : slot + 1;
+    for (int t = 0; t < ST; ++t)
+        send(t, t);
+    // Loads complete in order: with a row index each tile's are followed by one of indices.
+    // The indices that tile u needs were sent after tile u - 4, so the wait for tile t+1 in
+    // step t, which sends tile t + ST <= t + 4, covers them.
+    if (indexed)
+        wait_vm_then_sync<(ST - 1) * (LOADS + 1)>();
+    else
+        wait_vm_then_sync<(ST - 1) * LOADS>();
+    read(0, 0, I0{});
+    int slot = 0;
+    for (int t = 0; t < nk; ++t) {
+        const int next = slot + 1 == ST ? 0 : slot + 1;
+        read(slot, 1, I1{});
+        multiply(I0{}, I0{}, IE{});
+        read(slot, 2, I0{});
+        multiply(I1{}, I0{}, IE{});
+        read(slot, 3, I1{});
+        multiply(I0{}, I0{}, IE{});
+        multiply(I1{}, I0{}, IH{});
+        if (indexed)
+            wait_vm_then_sync<(ST - 2) * (LOADS + 1)>();
+        else
+            wait_vm_then_sync<(ST - 2) * LOADS>();
+        __builtin_amdgcn_sched_barrier(0);
+        send(t + ST, slot);
+        read(next, 0, I0{});
+        multiply(I1{}, IH{}, IE{});
+        slot = next;
     }
     wait_vm_then_sync<0>();
     // D: 32 rows at a time through LDS, 16 bytes per lane of whole row segments

@@ -18,8 +18,10 @@ hipError_t rows_tiled_nk(int dtype, Form form, const FusedArgs& p, int64_t tiles
     } while (0)
     switch (form) {
     case FORM_128: FORM(128, 128, 2, 2, 2, 2, 8); break;
+    case FORM_128_DEEP: FORM(128, 128, 2, 2, 4, 1, 8); break;
     case FORM_64: FORM(64, 128, 2, 2, 3, 2, 8); break;
-    default: FORM(64, 64, 2, 1, 3, 2, 8); break;
+    case FORM_SMALL: FORM(64, 64, 2, 1, 3, 2, 8); break;
+    default: FORM(64, 64, 2, 1, 8, 1, 8); break;
     }
 #undef FORM
 #undef TILED
