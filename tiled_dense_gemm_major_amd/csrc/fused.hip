@@ -158,8 +158,8 @@ tgemm_fused::Form choose_rows(const Layer& l) {
         double rate;                  // TB/s
     };
     static const Cost kCost[tgemm_fused::FORMS] = {
-        {1, 1.34, 1.34, 9, 5.1}, {2, 0.80, 0.97, 6, 4.6}, {1, 0.60, 0.60, 6, 4.6}, {2, 0.39, 0.68, 5, 4.6},
-        {3, 0.26, 0.45, 5, 4.6}, {1, 0.24, 0.24, 5, 4.6}, {2, 0.16, 0.30, 4, 5.5}, {4, 0.22, 0.55, 4, 5.6},
+        {1, 1.34, 1.34, 9, 5.1}, {1, 1.10, 1.10, 8, 5.0}, {2, 0.80, 0.97, 6, 4.6}, {1, 0.60, 0.60, 6, 4.6}, {2, 0.39, 0.68, 5, 4.6},
+        {3, 0.26, 0.58, 5, 4.6}, {1, 0.24, 0.24, 5, 4.6}, {2, 0.16, 0.30, 4, 5.5}, {4, 0.22, 0.55, 4, 5.6},
         {2, 0.18, 0.32, 4, 5.4}, {1, 0.24, 0.24, 4, 5.0}};
     // groups that have rows, if each row fell into any group alike
     const double live = l.groups == 1 ? 1.0 : l.groups * (1.0 - exp(-(double)l.rows / l.groups));
@@ -198,8 +198,9 @@ int launch_rows(const Layer& l, const FusedArgs& p, hipStream_t s) {
         (void)hipGetLastError();
         if (form >= tgemm_fused::FORM_STREAM16)
             return status(tgemm_fused::rows_stream(l.dtype, l.b_layout, form, p, tm, (int)tn, s));
-        if (form == tgemm_fused::FORM_QUAD)
-            return status(tgemm_fused::rows_quad(l.dtype, l.b_layout, p, tm, (int)tn, s));
+        if (form <= tgemm_fused::FORM_QUAD192)
+            return status(l.b_layout == TGEMM_B_NK ? tgemm_fused::rows_quad_nk(l.dtype, form, p, tm, (int)tn, s)
+                                                   : tgemm_fused::rows_quad_kn(l.dtype, form, p, tm, (int)tn, s));
         return status(l.b_layout == TGEMM_B_NK ? tgemm_fused::rows_tiled_nk(l.dtype, form, p, tm, (int)tn, s)
                                                : tgemm_fused::rows_tiled_kn(l.dtype, form, p, tm, (int)tn, s));
     }

@@ -238,8 +238,11 @@ __device__ __forceinline__ void unpack8(u32x4 v, float (&x)[8]) {
         x[e] = to_float<DT>(h[e]);
 }
 
-__device__ __forceinline__ u32x4 load8_raw(const u16* p, bool vec, int left) {
-    if (vec && left >= 8)
+// WHOLE: the caller has branched on the tensor's alignment and the run lying inside, so that
+// several loads go out together.
+template <bool WHOLE>
+__device__ __forceinline__ u32x4 load8_raw(const u16* p, int left) {
+    if constexpr (WHOLE)
         return *reinterpret_cast<const u32x4*>(p);
     u16x8 h;
 #pragma unroll
@@ -250,7 +253,7 @@ __device__ __forceinline__ u32x4 load8_raw(const u16* p, bool vec, int left) {
 
 template <int DT>
 __device__ __forceinline__ void load8(const u16* p, bool vec, int left, float (&x)[8]) {
-    unpack8<DT>(load8_raw(p, vec, left), x);
+    unpack8<DT>(vec && left >= 8 ? load8_raw<true>(p, left) : load8_raw<false>(p, left), x);
 }
 
 template <int DT>
@@ -622,20 +625,20 @@ __global__ void __launch_bounds__(256) slope_rows(const SlopeArgs p) {
     hi = hi < lo + kSliceRows ? hi : lo + kSliceRows;
     const int n = ((int)blockIdx.y * 64 + lane) * 8, left = width - n;
     float s0[8] = {0, 0, 0, 0, 0, 0, 0, 0}, s1[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (left > 0) {
-        // a wave's four rows: all loads before the arithmetic
+    // a wave's four rows: all loads before the arithmetic
+    auto rows = [&](auto wholec) {
+        constexpr bool WHOLE = decltype(wholec)::value;
         constexpr int R = kSliceRows / 4;
         u32x4 dy_raw[R], z_raw[R], u_raw[R];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const int r = lo + wave * R + i;
-            if (r < hi) {
-                dy_raw[i] = load8_raw(p.dC + (int64_t)r * p.lddc + n, p.vec, left);
-                if (p.Z)
-                    z_raw[i] = load8_raw(p.Z + (int64_t)r * p.ldz + n, p.vec, left);
-                if constexpr (GATED)
-                    u_raw[i] = load8_raw(p.Z + (int64_t)r * p.ldz + width + n, p.vec, left);
-            }
+            // a row past the slice reads the last one's values and is not used
+            const int64_t r = lo + wave * R + i < hi ? lo + wave * R + i : hi - 1;
+            dy_raw[i] = load8_raw<WHOLE>(p.dC + r * p.lddc + n, left);
+            if (p.Z)
+                z_raw[i] = load8_raw<WHOLE>(p.Z + r * p.ldz + n, left);
+            if constexpr (GATED)
+                u_raw[i] = load8_raw<WHOLE>(p.Z + r * p.ldz + width + n, left);
         }
 #pragma unroll
         for (int i = 0; i < R; ++i) {
@@ -663,12 +666,16 @@ __global__ void __launch_bounds__(256) slope_rows(const SlopeArgs p) {
             }
             if (p.dZ) {
                 u16* q = p.dZ + (int64_t)r * p.lddz + n;
-                store8<DT>(q, p.vec, left, z);
+                store8<DT>(q, WHOLE, left, z);
                 if constexpr (GATED)
-                    store8<DT>(q + width, p.vec, left, u);
+                    store8<DT>(q + width, WHOLE, left, u);
             }
         }
-    }
+    };
+    if (p.vec && left >= 8)
+        rows(std::true_type{});
+    else if (left > 0)
+        rows(std::false_type{});
     if (!p.sums)
         return;
 #pragma unroll

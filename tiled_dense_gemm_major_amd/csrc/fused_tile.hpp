@@ -295,16 +295,16 @@ fused_tiled(const FusedArgs p, int grid_n, int group_m) {
 }
 
 // ------------------------------------------------------------------------------------
-// The quad kernel over rows of groups: 256 x 256 tiles, one wave per SIMD with a 128 x 128
-// quadrant each, the library's main loop (quad_body) on a tile of a group.
+// The quad kernel over rows of groups: BMT x 256 tiles (BMT 256 or 192), one wave per SIMD
+// with a quadrant each, the library's main loop (quad_body) on a tile of a group.
 // ------------------------------------------------------------------------------------
-template <int DT>
+template <int DT, int BMT>
 struct QuadRows {
     static constexpr bool kActive = true;
     const FusedArgs& p;
     int g, row0, row_end, tn;
 
-    __device__ __forceinline__ int rows() const { return row_end - row0 < 256 ? row_end - row0 : 256; }
+    __device__ __forceinline__ int rows() const { return row_end - row0 < BMT ? row_end - row0 : BMT; }
     __device__ __forceinline__ int a_rows() const { return p.row_index ? p.a_rows : rows(); }
     __device__ __forceinline__ int a_row(int r) const { return p.row_index ? a_row_of(p, row0 + r) : r; }
     __device__ __forceinline__ int b_row(int c) const { return b_row_of<256>(p, tn, c); }
@@ -331,17 +331,17 @@ struct QuadRows {
     }
 };
 
-template <int DT, int MF, int LAYOUT, bool OFFS>
+template <int DT, int MF, int LAYOUT, bool OFFS, int BMT>
 __global__ void __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(1, 1)))
 fused_quad(const FusedArgs p, int grid_n, int group_m) {
     int g, row0, row_end, tn;
-    if (!find_tile<256>(p, (int)blockIdx.x, grid_n, group_m, g, row0, row_end, tn))
+    if (!find_tile<BMT>(p, (int)blockIdx.x, grid_n, group_m, g, row0, row_end, tn))
         return;
     g = __builtin_amdgcn_readfirstlane(g);
     row0 = __builtin_amdgcn_readfirstlane(row0);
     row_end = __builtin_amdgcn_readfirstlane(row_end);
-    const QuadRows<DT> hook{p, g, row0, row_end, tn};
-    quad_body<DT, MF, (MF == 16 ? 2 : 1), (MF == 16 ? 56 : 40), (MF == 16 ? 40 : 12), 1, 2, OFFS, LAYOUT, 256,
+    const QuadRows<DT, BMT> hook{p, g, row0, row_end, tn};
+    quad_body<DT, MF, (MF == 16 ? 2 : 1), (MF == 16 ? 56 : 40), (MF == 16 ? 40 : 12), 1, 2, OFFS, LAYOUT, BMT,
               LAYOUT_MK, 0>(p.row_index ? p.A : p.A + (int64_t)row0 * p.lda, p.B + (int64_t)g * p.stride_b, nullptr,
                             hook.rows(), p.N, p.K, p.lda, p.ldb, 0, 0, tn, 0, 0, nullptr, 0, 0, 0, false, hook);
 }

@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(256) route_grad(const RouteGradArgs p) {
 // one workgroup does all of it; beyond, plan_count writes the count of each chunk of
 // choices and plan_place, one workgroup per chunk, adds up the chunks before its own.
 // ------------------------------------------------------------------------------------
-constexpr int kPlanChunk = 4096, kPlanWaves = 16;
+constexpr int kPlanChunk = 4096, kPlanWaves = 16;   // one workgroup's choices, its waves
 
 struct PlanArgs {
     const int32_t* ids;
@@ -693,21 +693,41 @@ __global__ void __launch_bounds__(256) combine_rows(const CombineArgs p) {
     if (t >= p.tokens)
         return;
     const int n = (int)(q - t * runs) * 8, left = p.width - n;
-    float y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (p.residual)
-        load8<DT>(p.residual + t * p.ldr + n, p.vec, left, y);
-    for (int j = 0; j < p.k; ++j) {
-        const int slot = p.slots[t * p.k + j];
-        if (slot < 0 || slot >= p.rows)
-            continue;
-        const float w = p.weights ? p.weights[t * p.k + j] : 1.0f;
-        float o[8];
-        load8<DT>(p.O + (int64_t)slot * p.ldo + n, p.vec, left, o);
+    auto sum = [&](auto wholec) {
+        constexpr bool WHOLE = decltype(wholec)::value;
+        float y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (p.residual)
+            unpack8<DT>(load8_raw<WHOLE>(p.residual + t * p.ldr + n, left), y);
+        // four choices' loads at a time
+        for (int j0 = 0; j0 < p.k; j0 += 4) {
+            u32x4 o_raw[4];
+            float w[4];
+            bool live[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            y[e] = fmaf(w, o[e], y[e]);
-    }
-    store8<DT>(p.Y + t * p.ldy + n, p.vec, left, y);
+            for (int q = 0; q < 4; ++q) {
+                const int64_t c = t * p.k + (j0 + q < p.k ? j0 + q : p.k - 1);
+                const int slot = p.slots[c];
+                live[q] = j0 + q < p.k && slot >= 0 && slot < p.rows;
+                w[q] = p.weights ? p.weights[c] : 1.0f;
+                if (live[q])
+                    o_raw[q] = load8_raw<WHOLE>(p.O + (int64_t)slot * p.ldo + n, left);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (live[q]) {
+                    float o[8];
+                    unpack8<DT>(o_raw[q], o);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        y[e] = fmaf(w[q], o[e], y[e]);
+                }
+        }
+        store8<DT>(p.Y + t * p.ldy + n, WHOLE, left, y);
+    };
+    if (p.vec && left >= 8)
+        sum(std::true_type{});
+    else
+        sum(std::false_type{});
 }
 
 // Its backward pass: dO[slot[t,j]] = w[t,j] dY[t] and dw[t,j] = <dY[t], O[slot[t,j]]>, one
@@ -736,12 +756,17 @@ __global__ void __launch_bounds__(256) combine_grad(const CombineGradArgs p) {
     float dot = 0.0f;
     if (live) {
         const float w = p.weights ? p.weights[c] : 1.0f;
-        for (int n = lane * 8; n < p.width; n += 512) {
+        auto run = [&](auto wholec, int n) {
+            constexpr bool WHOLE = decltype(wholec)::value;
             const int left = p.width - n;
             float dy[8], o[8];
-            load8<DT>(p.dY + t * p.lddy + n, p.vec, left, dy);
+            u32x4 o_raw{};
+            const u32x4 dy_raw = load8_raw<WHOLE>(p.dY + t * p.lddy + n, left);
+            if (p.dw)
+                o_raw = load8_raw<WHOLE>(p.O + (int64_t)slot * p.ldo + n, left);
+            unpack8<DT>(dy_raw, dy);
             if (p.dw) {
-                load8<DT>(p.O + (int64_t)slot * p.ldo + n, p.vec, left, o);
+                unpack8<DT>(o_raw, o);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     dot = fmaf(dy[e], o[e], dot);
@@ -750,8 +775,14 @@ __global__ void __launch_bounds__(256) combine_grad(const CombineGradArgs p) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     dy[e] *= w;
-                store8<DT>(p.dO + (int64_t)slot * p.lddo + n, p.vec, left, dy);
+                store8<DT>(p.dO + (int64_t)slot * p.lddo + n, WHOLE, left, dy);
             }
+        };
+        for (int n = lane * 8; n < p.width; n += 512) {
+            if (p.vec && n + 8 <= p.width)
+                run(std::true_type{}, n);
+            else
+                run(std::false_type{}, n);
         }
     }
     if (p.dw) {
