@@ -380,8 +380,11 @@ int gemm_fused(int dtype, int64_t m, int64_t n, int64_t k, const void* A, int64_
  *                address and stride).  Not used without an activation and a gate, nor when
  *                neither dA nor dB is wanted
  *   dbias      : from the unrounded dZ, summed in a fixed order
- *   workspace  : needed with dbias, gemm_backward_workspace_size(1, m, n) bytes, 16-byte
- *                aligned; else ignored
+ *   workspace  : 16-byte aligned; needed with dbias, for whose sums
+ *                gemm_backward_workspace_size(1, m, n, 0, 1, ..) bytes must be there.  With
+ *                gemm_backward_workspace_size(1, m, n, k, ..) bytes a dB of few tiles over
+ *                many rows is summed in parts, which is faster; without, it is summed whole.
+ *                Two calls in flight may not share one
  * Errors as gemm_fused, and TGEMM_ERR_WORKSPACE.
  */
 int gemm_fused_backward(int dtype, int64_t m, int64_t n, int64_t k, const void* dC,
@@ -391,9 +394,11 @@ int gemm_fused_backward(int dtype, int64_t m, int64_t n, int64_t k, const void* 
                         int64_t lddb, float* dbias, void* workspace, int64_t workspace_bytes,
                         void* stream);
 
-/* Workspace bytes of gemm_fused_backward (groups 1) and gemm_grouped_backward with dbias.
+/* The workspace bytes that gemm_fused_backward (groups 1) and gemm_grouped_backward can use:
+ * dbias 1 with the bias's sums (0: without), k > 0 with the parts of dB (k 0: without).
  * Host-only. */
-int gemm_backward_workspace_size(int64_t groups, int64_t rows, int64_t n, int64_t* bytes);
+int gemm_backward_workspace_size(int64_t groups, int64_t rows, int64_t n, int64_t k, int dbias,
+                                 int64_t* bytes);
 
 /*
  * One product per group of rows, each with its own B (and bias), as the experts of a

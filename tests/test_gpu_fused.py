@@ -355,3 +355,24 @@ def test_rows_past_32_bits(tg):
     tg.gemm_fused(A, B, C, activation=ACT_RELU, residual=C)
     want = 2 * (A.double() @ B.double().t()).clamp(min=0)
     assert_within(C, want, 2 * half_step(dt, want), "far rows")
+
+
+@pytest.mark.parametrize("layout", [0, 1])
+@pytest.mark.parametrize("m,n,k", [(8192, 128, 136), (5000, 264, 64), (2049, 72, 520)])
+def test_backward_of_many_rows_in_parts(tg, m, n, k, layout):
+    """dB of few tiles over many rows: summed in parts with the whole workspace, whole with
+    the bias's alone or none; nothing outside the workspace is written."""
+    dt = torch.bfloat16
+    A, B = eighths((m, k), 101, dt), _b(n, k, layout, 102, dt, tg)
+    dC = eighths((m, n), 103, dt)
+    full, bias_only = tg.backward_workspace_size(m, n, k), tg.backward_workspace_size(m, n)
+    assert full > bias_only, "these sizes are to be summed in parts"
+    for size in (full, bias_only):
+        buf = torch.full((size + 512,), 165, dtype=torch.uint8, device="cuda")
+        ws = buf[256:256 + size]
+        got = tg.gemm_fused_backward(dC.cuda(), A.cuda(), B.cuda(), b_layout=layout, dA=False, dbias=True,
+                                     workspace=ws)
+        _check_gradients(tg, A, B, layout, dC, dC, ACT_NONE, False, got, None, f"workspace {size}")
+        assert bool((buf[:256] == 165).all()) and bool((buf[256 + size:] == 165).all())
+    again = tg.gemm_fused_backward(dC.cuda(), A.cuda(), B.cuda(), b_layout=layout, dA=False, dbias=True)
+    assert torch.equal(again[1], tg.gemm_fused_backward(dC.cuda(), A.cuda(), B.cuda(), b_layout=layout, dA=False)[1])

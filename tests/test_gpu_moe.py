@@ -320,6 +320,25 @@ def test_grouped_offsets_out_of_order(tg, k):
         assert bool((C[~done] == 9.0).all())
 
 
+def test_grouped_backward_offsets_out_of_order(tg):
+    """Groups that overlap through descending offsets have more slices than any ascending
+    ones: nothing is read or written outside the tensors and the workspace."""
+    dt, rows, n, k = torch.float16, 90, 40, 24
+    A, B = eighths((rows, k), 1, dt).cuda(), eighths((6, n, k), 2, dt, top=2).cuda()
+    dC, Z = eighths((rows, n), 3, dt).cuda(), eighths((rows, n), 4, dt).cuda()
+    offsets = torch.tensor([0, 90, 0, 90, 0, 90, -5], dtype=torch.int32, device="cuda")
+    size = tg.backward_workspace_size(rows, n, k, groups=6)
+    buf = torch.full((size + 512,), 165, dtype=torch.uint8, device="cuda")
+    dA = torch.full((rows + 20, k), 9.0, dtype=dt, device="cuda")
+    dB = torch.full((8, n, k), 9.0, dtype=dt, device="cuda")
+    tg.gemm_grouped_backward(dC, A, B, offsets, Z, activation=ACT_RELU, dA=dA[10:10 + rows], dB=dB[1:7], dbias=True,
+                             workspace=buf[256:256 + size])
+    assert bool((buf[:256] == 165).all()) and bool((buf[256 + size:] == 165).all())
+    assert bool((dA[:10] == 9.0).all()) and bool((dA[10 + rows:] == 9.0).all())
+    assert bool((dB[0] == 9.0).all()) and bool((dB[7] == 9.0).all())
+    assert not dB[2].any() and not dB[4].any()          # the groups whose end lies before their start
+
+
 def _check_grouped_gradients(tg, A, B, layout, offsets, index, div, Z, dC, kind, gated, got, dZ, used, what):
     dA, dB, dbias = got
     dt = A.dtype

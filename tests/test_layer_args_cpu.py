@@ -82,6 +82,7 @@ def _backward(lib, m=16, n=32, k=64, act=4, gated=0, dC=FAKE, lddc=32, A=FAKE + 
     (ALIAS, dict(dZ=FAKE)), (ALIAS, dict(dZ=FAKE + 3 * G + 2)), (ALIAS, dict(dA=FAKE + G)),
     (ALIAS, dict(dB=FAKE + 2 * G)), (ALIAS, dict(dA=FAKE + 4 * G)), (ALIAS, dict(dbias=FAKE + 5 * G)),
     (ALIAS, dict(ws=FAKE + 6 * G)), (ALIAS, dict(dB=FAKE + 3 * G)),
+    (ALIGN, dict(dbias=None, ws=FAKE + 8 * G + 8)), (ALIAS, dict(dbias=None, ws=FAKE + 5 * G)),
 ])
 def test_backward_refusals(lib, want, change):
     assert _backward(lib, **change) == want
@@ -177,9 +178,15 @@ def test_workspace_sizes(lib):
     # one row of n floats per 64 rows of a group, whatever the groups' ends
     assert tgemm.backward_workspace_size(1000, 64) >= 16 * 64 * 4
     assert tgemm.backward_workspace_size(1000, 64, groups=10) >= (15 + 10) * 64 * 4
+    assert tgemm.backward_workspace_size(1000, 64, dbias=False) == 0
+    # few tiles over many rows: room for the parts of dB, within 64 MiB
+    assert 0 < tgemm.backward_workspace_size(8192, 1024, 1024, dbias=False) <= 64 << 20
+    assert tgemm.backward_workspace_size(4096, 8192, 4096, dbias=False) == 0
     n = ctypes.c_int64()
     assert lib.moe_plan_workspace_size(1, 1, None) == NULL
-    assert lib.gemm_backward_workspace_size(0, 1, 1, ctypes.byref(n)) == INVALID
+    assert lib.gemm_backward_workspace_size(0, 1, 1, 1, 0, ctypes.byref(n)) == INVALID
+    assert lib.gemm_backward_workspace_size(1, 1, 1, 1, 2, ctypes.byref(n)) == INVALID
+    assert lib.gemm_backward_workspace_size(1, 1, 1, 1, 1, None) == NULL
 
 
 def test_binding_refuses_what_it_cannot_pass():

@@ -19,7 +19,9 @@ __global__ void __launch_bounds__(1024) bias_sum(const SlopeArgs p, float* __res
     int lo, hi;
     group_rows(p, g, lo, hi);
     const int first = slices_before(p, g), count = (hi - lo + kSliceRows - 1) / kSliceRows;
-    const int b = first + (int)((int64_t)wave * count / 16), e = first + (int)((int64_t)(wave + 1) * count / 16);
+    const int b = first + (int)((int64_t)wave * count / 16);
+    int e = first + (int)((int64_t)(wave + 1) * count / 16);
+    e = e < p.slices ? e : p.slices;       // groups that overlap (offsets out of order) have more
     float t = 0.0f;
     if (n < p.N) {
 #pragma unroll 8
@@ -316,33 +318,60 @@ struct Gradients {
 };
 
 // The form of a sum over rows, by the same estimate: rounds of workgroups times steps of 64
-// rows times the time of a step.
-tgemm_fused::SumForm choose_sum(const Layer& l, const SumArgs& p, bool quad) {
+// rows times the time of a step; and the number of ranges that a group's rows are cut into
+// where the 128 x 128 tiles leave compute units idle (fp32 partial tiles, written and read
+// once: 8192 rows to 1024 x 1024 77 us whole).  Parts of 256 rows or more, at most 16, and
+// at most kMaxPartialBytes of them.
+struct SumPlan {
+    tgemm_fused::SumForm form;
+    int parts;
+};
+constexpr int64_t kMaxPartialBytes = int64_t(64) << 20;
+
+SumPlan choose_sum(int64_t groups, int64_t rows, int64_t I, int64_t J, bool quad, bool split) {
     struct Cost {
         int per_unit;
         double alone, shared, fixed;
     };
     static const Cost kCost[tgemm_fused::SUM_FORMS] = {
         {1, 1.43, 1.43, 8}, {1, 1.75, 1.75, 9}, {2, 0.72, 1.05, 6}, {2, 0.5, 0.55, 5}};
-    const double steps = (double)cdiv(cdiv(l.rows, l.groups), 64);
-    int best = 1;
-    double least = 0;
-    for (int f = quad ? 0 : 1; f < tgemm_fused::SUM_FORMS; ++f) {
+    const double steps = (double)cdiv(cdiv(rows, groups), 64);
+    const auto cost_of = [&](int f, int64_t parts) {
         const int t = tgemm_fused::kSumTiles[f];
-        const double tiles = (double)(l.groups * cdiv(p.I, t) * cdiv(p.J, t));
+        const double tiles = (double)(groups * cdiv(I, t) * cdiv(J, t) * parts);
         const Cost& c = kCost[f];
         const double slots = 256.0 * c.per_unit, full = floor(tiles / slots), rest = tiles - full * slots;
-        const double cost = steps * (full * c.shared + (rest > 256 ? c.shared : (rest > 0 ? c.alone : 0))) +
-                            c.fixed * (full + (rest > 0));
-        if (f == (quad ? 0 : 1) || cost < least) {
-            best = f;
-            least = cost;
+        return ceil(steps / parts) * (full * c.shared + (rest > 256 ? c.shared : (rest > 0 ? c.alone : 0))) +
+               c.fixed * (full + (rest > 0));
+    };
+    SumPlan best{tgemm_fused::SUM_256, 1};
+    double least = cost_of(tgemm_fused::SUM_256, 1);
+    for (int f = 0; f < tgemm_fused::SUM_FORMS; ++f)
+        if (f != tgemm_fused::SUM_256 && (f != tgemm_fused::SUM_QUAD || quad) && cost_of(f, 1) < least) {
+            best.form = (tgemm_fused::SumForm)f;
+            least = cost_of(f, 1);
         }
-    }
-    return (tgemm_fused::SumForm)best;
+    const int64_t tiles = groups * cdiv(I, 128) * cdiv(J, 128);
+    if (split && tiles > 0 && tiles < 256)
+        for (int64_t parts = 2; parts <= 16 && parts * tiles <= 512 && steps / parts >= 4; ++parts) {
+            const double bytes = 4.0 * parts * groups * I * J;
+            if (bytes > (double)kMaxPartialBytes)
+                break;
+            const double cost = cost_of(tgemm_fused::SUM_128, parts) + 4 + 2 * bytes / 4.6e6;
+            if (cost < least) {
+                best = {tgemm_fused::SUM_128, (int)parts};
+                least = cost;
+            }
+        }
+    return best;
 }
 
-int launch_sum(const Layer& l, const SumArgs& p, hipStream_t s) {
+int64_t partial_bytes(const SumPlan& plan, int64_t groups, int64_t I, int64_t J) {
+    return plan.parts > 1 ? 4 * plan.parts * groups * I * J : 0;
+}
+
+// `partial`: workspace for the parts' sums, 16-byte aligned, or null.
+int launch_sum(const Layer& l, SumArgs p, float* partial, int64_t bytes, hipStream_t s) {
     const auto through = [&](bool indexed, int64_t cols, int64_t ld) {
         return ld <= (int64_t(1) << 23) && cols % 8 == 0 && ld % 8 == 0 &&
                (!indexed || 2 * span(p.a_rows, cols, ld) <= kMaxBufferBytes);
@@ -352,11 +381,16 @@ int launch_sum(const Layer& l, const SumArgs& p, hipStream_t s) {
             return TGEMM_ERR_UNSUPPORTED;
         const bool quad = !p.row_index && p.vec && 2 * span(p.rows, p.I, p.ldl) <= kMaxBufferBytes &&
                           2 * span(p.rows, p.J, p.ldr) <= kMaxBufferBytes;
-        const tgemm_fused::SumForm form = choose_sum(l, p, quad);
+        SumPlan plan = choose_sum(l.groups, l.rows, p.I, p.J, quad, partial != nullptr);
+        if (partial_bytes(plan, l.groups, p.I, p.J) > bytes)
+            plan = choose_sum(l.groups, l.rows, p.I, p.J, quad, false);
+        p.partial = partial;
+        p.parts = plan.parts;
         (void)hipGetLastError();
-        return status(form == tgemm_fused::SUM_QUAD ? tgemm_fused::sum_quad(l.dtype, p, s)
-                                                    : tgemm_fused::sum_tiled(l.dtype, form, p, s));
+        return status(plan.form == tgemm_fused::SUM_QUAD ? tgemm_fused::sum_quad(l.dtype, p, s)
+                                                         : tgemm_fused::sum_tiled(l.dtype, plan.form, p, s));
     }
+    p.parts = 1;
     const int64_t gi = cdiv(p.I, 64), gj = cdiv(p.J, 64);
     if (l.groups * gi * gj > kMaxDim)
         return TGEMM_ERR_UNSUPPORTED;
@@ -403,13 +437,15 @@ int backward(const Layer& l, const Gradients& d, void* stream) {
         return TGEMM_ERR_ALIGNMENT;
     if ((uintptr_t)d.dbias % 4)
         return TGEMM_ERR_ALIGNMENT;
+    // the workspace: the bias's sums, then (as much as is there) the parts of dB's
     const int64_t sums_bytes = d.dbias ? 4 * most_slices(l.groups, l.rows) * l.n : 0;
-    if (sums_bytes > 0) {
-        if (!d.workspace || d.workspace_bytes < sums_bytes)
-            return TGEMM_ERR_WORKSPACE;
-        if (!al16(d.workspace))
-            return TGEMM_ERR_ALIGNMENT;
-    }
+    if (sums_bytes > 0 && (!d.workspace || d.workspace_bytes < sums_bytes))
+        return TGEMM_ERR_WORKSPACE;
+    if (!al16(d.workspace))
+        return TGEMM_ERR_ALIGNMENT;
+    const int64_t parts_at = cdiv(sums_bytes, 16) * 16;
+    const bool lent = d.workspace && d.dB && d.workspace_bytes > parts_at;
+    float* parts = lent ? static_cast<float*>(d.workspace) + parts_at / 4 : nullptr;
     const Extent in[] = {{d.dC, 2 * span(l.rows, l.width(), d.lddc)},
                          {slope ? d.Z : nullptr, 2 * span(l.rows, l.n, d.ldz)},
                          l.a(),
@@ -421,7 +457,7 @@ int backward(const Layer& l, const Gradients& d, void* stream) {
         {d.dA, 2 * span(l.rows, l.k, d.ldda)},
         {d.dB, 2 * ((l.groups - 1) * d.stride_db + span(l.b_rows(), l.b_cols(), d.lddb))},
         {d.dbias, 4 * l.groups * l.n},
-        {d.workspace, sums_bytes}};
+        {d.workspace, lent ? d.workspace_bytes : sums_bytes}};
     for (int i = 0; i < 5; ++i) {
         for (int j = 0; j < 6; ++j) {
             // dZ may take Z's place: each value is read before it is written
@@ -454,6 +490,7 @@ int backward(const Layer& l, const Gradients& d, void* stream) {
         p.vec = al16(d.dC) && d.lddc % 8 == 0 && (!p.Z || (al16(d.Z) && d.ldz % 8 == 0)) &&
                 (!p.dZ || (al16(d.dZ) && d.lddz % 8 == 0)) && l.width() % 8 == 0;
         const int64_t slices = l.offsets ? most_slices(l.groups, l.rows) : cdiv(l.rows, tgemm::kSliceRows);
+        p.slices = (int)slices;
         const int64_t columns = cdiv(l.width(), 512);
         if (columns > 65535)
             return TGEMM_ERR_UNSUPPORTED;
@@ -527,7 +564,7 @@ int backward(const Layer& l, const Gradients& d, void* stream) {
         p.index_left = l.row_index && !nk;
         p.index_right = l.row_index && nk;
         p.vec = al16(d.dB) && d.lddb % 8 == 0 && (l.groups == 1 || d.stride_db % 8 == 0);
-        rc = launch_sum(l, p, s);
+        rc = launch_sum(l, p, parts, lent ? d.workspace_bytes - parts_at : 0, s);
     }
     return rc;
 }
@@ -558,14 +595,22 @@ int gemm_grouped(int dtype, int64_t groups, int64_t rows, int64_t n, int64_t k, 
                    C, ldc, e, stream);
 }
 
-int gemm_backward_workspace_size(int64_t groups, int64_t rows, int64_t n, int64_t* bytes) {
+int gemm_backward_workspace_size(int64_t groups, int64_t rows, int64_t n, int64_t k, int dbias, int64_t* bytes) {
     if (!bytes)
         return TGEMM_ERR_NULL_POINTER;
-    if (groups < 1 || rows < 0 || n < 0)
+    if (groups < 1 || rows < 0 || n < 0 || k < 0 || (dbias != 0 && dbias != 1))
         return TGEMM_ERR_INVALID_VALUE;
-    if (groups > 65535 || rows > kMaxDim || n > kMaxDim)
+    if (groups > 65535 || rows > kMaxDim || n > kMaxDim || k > kMaxDim)
         return TGEMM_ERR_UNSUPPORTED;
-    *bytes = 4 * most_slices(groups, rows) * n;
+    const int64_t sums = dbias ? cdiv(4 * most_slices(groups, rows) * n, 16) * 16 : 0;
+    // the parts' sums, for whichever of the forms a call may choose from
+    int64_t parts = 0;
+    if (rows > 0 && n > 0 && k > 0)
+        for (int quad = 0; quad < 2; ++quad) {
+            const int64_t b = partial_bytes(choose_sum(groups, rows, n, k, quad != 0, true), groups, n, k);
+            parts = b > parts ? b : parts;
+        }
+    *bytes = sums + parts;
     return TGEMM_OK;
 }
 

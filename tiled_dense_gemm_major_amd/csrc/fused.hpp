@@ -479,6 +479,8 @@ struct SumArgs {
     int32_t I, J, ldl, ldr, ldd;
     int32_t index_left, index_right;   // which of the two goes through the row index
     int32_t vec;                       // D takes 16-byte stores at multiples of 8
+    float* partial;                    // parts > 1: [parts][groups][I][J] sums of row ranges
+    int32_t parts;
 };
 
 __device__ __forceinline__ void group_rows(const SumArgs& p, int g, int& lo, int& hi) {
@@ -558,6 +560,7 @@ struct SlopeArgs {
     const u16* Z;          // null: act none, not gated
     u16* dZ;               // null: dZ is not wanted (it equals dC)
     float* sums;           // [slices][N], or null
+    int32_t slices;        // rows of the workspace: no group's slices reach past them
     const int32_t* offsets;
     int32_t rows, groups, N, lddc, ldz, lddz, act, gated;
     int32_t vec;           // dC, Z, dZ all take 16-byte accesses

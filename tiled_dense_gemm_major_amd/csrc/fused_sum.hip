@@ -9,7 +9,7 @@ hipError_t sum_tiled(int dtype, SumForm form, const SumArgs& p, hipStream_t s) {
     do {                                                                                   \
         const int gi = (p.I + BI - 1) / BI, gj = (p.J + BJ - 1) / BJ;                      \
         hipLaunchKernelGGL((tgemm::sum_tiled<DT, BI, BJ, WI, WJ, ST, OCC>),                \
-                           dim3((unsigned)((int64_t)p.groups * gi * gj)), dim3(WI * WJ * 64), 0, s, p, gi, gj); \
+                           dim3((unsigned)((int64_t)p.groups * p.parts * gi * gj)), dim3(WI * WJ * 64), 0, s, p, gi, gj); \
     } while (0)
 #define FORM(BI, BJ, WI, WJ, ST, OCC)                                                      \
     do {                                                                                   \
@@ -25,6 +25,14 @@ hipError_t sum_tiled(int dtype, SumForm form, const SumArgs& p, hipStream_t s) {
     }
 #undef FORM
 #undef SUM
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.parts == 1)
+        return e;
+    const dim3 grid((unsigned)(((int64_t)p.groups * p.I * (p.J / 8) + 255) / 256));
+    if (dtype == tgemm::DT_F16)
+        hipLaunchKernelGGL((tgemm::sum_parts<0>), grid, dim3(256), 0, s, p);
+    else
+        hipLaunchKernelGGL((tgemm::sum_parts<1>), grid, dim3(256), 0, s, p);
     return hipGetLastError();
 }
 

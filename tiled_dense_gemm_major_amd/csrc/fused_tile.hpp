@@ -367,6 +367,8 @@ sum_quad(const SumArgs p, int grid_i, int grid_j) {
 // reads.  With a row index, each tile's 64 indices come by a direct-to-LDS load of their own
 // into a ring of four, four tiles before the tile whose loads need them (so that they are
 // there by the wait for an older tile).
+//   parts > 1 (few tiles, many rows): the rows of a group are cut into as many ranges, one
+// workgroup each, whose fp32 tiles go to the workspace; sum_parts adds them in order.
 // ------------------------------------------------------------------------------------
 __device__ __forceinline__ void dma4_at(rsrc4_t r, uint32_t lds_byte, uint32_t voff) {
     const uint32_t m0v = __builtin_amdgcn_readfirstlane(lds_byte);
@@ -385,10 +387,16 @@ sum_tiled(const SumArgs p, int grid_i, int grid_j) {
     static_assert(NW * 32 * SRS <= ST * STAGE, "D staging fits the ring");
     __shared__ __attribute__((aligned(1024))) u16 lds[ST * STAGE];
     __shared__ __attribute__((aligned(256))) int32_t idx[NW][4][64];
-    const int per = grid_i * grid_j, g = (int)blockIdx.x / per;
+    const int per = grid_i * grid_j, gp = (int)blockIdx.x / per, g = gp % p.groups, part = gp / p.groups;
     int ti, tj, lo, hi;
     tile_of((int)blockIdx.x % per, grid_i, grid_j, 4, ti, tj);
     group_rows(p, g, lo, hi);
+    if (p.parts > 1) {                                  // whole tiles of 64 rows to each part
+        const int tiles = (hi - lo + kTileK - 1) / kTileK, first = lo;
+        lo = first + (int)((int64_t)part * tiles / p.parts) * kTileK;
+        const int end = first + (int)((int64_t)(part + 1) * tiles / p.parts) * kTileK;
+        hi = end < hi ? end : hi;
+    }
     lo = __builtin_amdgcn_readfirstlane(lo);
     hi = __builtin_amdgcn_readfirstlane(hi);
     const int tid = (int)threadIdx.x, lane = tid & 63;
@@ -517,6 +525,25 @@ sum_tiled(const SumArgs p, int grid_i, int grid_j) {
         slot = next;
     }
     wait_vm_then_sync<0>();
+    if (p.parts > 1) {
+        // a lane's four consecutive columns of one row are one 16-byte store
+        float* P = p.partial + (int64_t)gp * p.I * p.J;
+#pragma unroll
+        for (int i = 0; i < TI; ++i) {
+            const int row = ti * BI + wi * WTI + 32 * i + lr;
+#pragma unroll
+            for (int j = 0; j < TJ; ++j)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const int col = tj * BJ + wj * WTJ + 32 * j + 8 * v + 4 * half;
+                    if (row < p.I && col < p.J)         // J is a multiple of 8
+                        *reinterpret_cast<f32x4*>(P + (int64_t)row * p.J + col) =
+                            f32x4{acc[i][j][4 * v], acc[i][j][4 * v + 1], acc[i][j][4 * v + 2],
+                                  acc[i][j][4 * v + 3]};
+                }
+        }
+        return;
+    }
     // D: 32 rows at a time through LDS, 16 bytes per lane of whole row segments
     u16* stage = lds + wave * 32 * SRS;
     constexpr int RUNS = WTJ / 8, RPI = 64 / RUNS;
@@ -551,6 +578,31 @@ sum_tiled(const SumArgs p, int grid_i, int grid_j) {
             }
         }
     }
+}
+
+// The parts' sums in order, eight columns of one row per thread, rounded once.
+template <int DT>
+__global__ void __launch_bounds__(256) sum_parts(const SumArgs p) {
+    const int64_t runs = p.J / 8, q = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t plane = (int64_t)p.groups * p.I * p.J;
+    if (q >= (int64_t)p.groups * p.I * runs)
+        return;
+    const int64_t row = q / runs;                       // group * I + i
+    const int j = (int)(q - row * runs) * 8;
+    const float* src = p.partial + row * p.J + j;
+    float t[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 4
+    for (int part = 0; part < p.parts; ++part) {
+        const f32x4 a = *reinterpret_cast<const f32x4*>(src + part * plane);
+        const f32x4 b = *reinterpret_cast<const f32x4*>(src + part * plane + 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            t[e] += a[e];
+            t[4 + e] += b[e];
+        }
+    }
+    const int g = (int)(row / p.I), i = (int)(row - (int64_t)g * p.I);
+    store8<DT>(p.D + (int64_t)g * p.stride_d + (int64_t)i * p.ldd + j, p.vec, 8, t);
 }
 
 }  // namespace tgemm

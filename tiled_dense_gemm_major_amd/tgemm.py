@@ -128,7 +128,7 @@ def load(path: str = LIB_PATH):
     lib.gemm_grouped_backward.argtypes = [i32, i64, i64, i64, i64, vp, vp, i64, vp, i64, vp,
                                           i64, i64, vp, i64, i64, i32, i32, i32, vp, i64, vp,
                                           i64, vp, i64, vp, i64, i64, vp, vp, i64, vp]
-    lib.gemm_backward_workspace_size.argtypes = [i64, i64, i64, i64p]
+    lib.gemm_backward_workspace_size.argtypes = [i64, i64, i64, i64, i32, i64p]
     lib.moe_route.argtypes = [i32, i64, i64, i64, vp, i64, vp, i32, i64, i64, i32, i32, f32, vp,
                               vp, vp]
     lib.moe_route_backward.argtypes = [i32, i64, i64, i64, vp, i64, vp, vp, i32, i32, f32, vp,
@@ -464,10 +464,12 @@ def gemm_fused(A, B, C=None, b_layout=B_NK, bias=None, activation=ACT_NONE, gate
     return C
 
 
-def backward_workspace_size(rows, n, groups=1) -> int:
-    """Workspace bytes of a backward call with dbias."""
+def backward_workspace_size(rows, n, k=0, groups=1, dbias=True) -> int:
+    """Workspace bytes that a backward call can use: needed with dbias, and with k > 0 those
+    that let a dB of few tiles over many rows be summed in parts."""
     nbytes = ctypes.c_int64(0)
-    _check(load().gemm_backward_workspace_size(groups, rows, n, ctypes.byref(nbytes)),
+    _check(load().gemm_backward_workspace_size(groups, rows, n, k, int(bool(dbias)),
+                                               ctypes.byref(nbytes)),
            "gemm_backward_workspace_size")
     return int(nbytes.value)
 
@@ -479,7 +481,7 @@ def _gradient(t, like, shape, dtype=None):
     return like.new_empty(shape, dtype=dtype or like.dtype) if t is True else t
 
 
-def _gradient_buffers(A, rows, n, groups, activation, gated, preact, dZ, products, dbias,
+def _gradient_buffers(A, rows, n, k, groups, activation, gated, preact, dZ, dA, dB, dbias,
                       workspace):
     """(preact address and stride, dZ address and stride, workspace address and bytes)."""
     z = zs = d = ds = w = wb = 0
@@ -487,15 +489,17 @@ def _gradient_buffers(A, rows, n, groups, activation, gated, preact, dZ, product
         if preact is None:
             raise ValueError("preact is needed with an activation or a gate")
         z, _, _, zs = _matrix(preact, "preact", A, (rows, n))
-        if products:
+        if dA is not None or dB is not None:
             if dZ is None:
                 dZ = A.new_empty((rows, n))
             d, _, _, ds = _matrix(dZ, "dZ", A, (rows, n))
-    if dbias is not None:
-        wb = backward_workspace_size(rows, n, groups)
-        if workspace is None:
-            workspace = A.new_empty((max(wb, 16),), dtype=_torch()[0].uint8)
-        elif workspace.get_device() != A.get_device() or not workspace.is_contiguous():
+    if workspace is None:
+        wb = backward_workspace_size(rows, n, 0 if dB is None else k, groups, dbias is not None)
+        if wb:
+            workspace = A.new_empty((wb,), dtype=_torch()[0].uint8)
+            w = workspace.data_ptr()
+    else:
+        if workspace.get_device() != A.get_device() or not workspace.is_contiguous():
             raise ValueError("the workspace must be contiguous and on the operands' GPU")
         w, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     # the tensors allocated here are kept until the call has been enqueued
@@ -520,8 +524,7 @@ def gemm_fused_backward(dC, A, B, preact=None, b_layout=B_NK, activation=ACT_NON
     db, _, _, lddb = (0, 0, 0, 0) if dB is None else _matrix(dB, "dB", A, (b_rows, b_cols))
     dbv = 0 if dbias is None else _vector(dbias, "dbias", A, torch.float32, n)
     z, ldz, d, lddz, w, wb, keep = _gradient_buffers(
-        A, m, n, 1, activation, gated, preact, dZ, dA is not None or dB is not None, dbias,
-        workspace)
+        A, m, n, k, 1, activation, gated, preact, dZ, dA, dB, dbias, workspace)
     _launch("gemm_fused_backward", A, stream, dtype, m, n, k, dc, lddc, a, lda, b, ldb, b_layout,
             activation, int(bool(gated)), z, ldz, d, lddz, da, ldda, db, lddb, dbv, w, wb)
     return dA, dB, dbias
@@ -593,8 +596,7 @@ def gemm_grouped_backward(dC, A, B, offsets, preact=None, row_index=None, row_di
     db, lddb, stride_db = (0, 0, 0) if dB is None else _stack(dB, "dB", A, b_shape)
     dbv = 0 if dbias is None else _vector(dbias, "dbias", A, torch.float32, groups * n)
     z, ldz, d, lddz, w, wb, keep = _gradient_buffers(
-        A, rows, n, groups, activation, gated, preact, dZ, dA is not None or dB is not None,
-        dbias, workspace)
+        A, rows, n, k, groups, activation, gated, preact, dZ, dA, dB, dbias, workspace)
     _launch("gemm_grouped_backward", A, stream, dtype, groups, rows, n, k, off, idx, row_div, dc,
             lddc, a, a_rows, lda, b, ldb, stride_b, b_layout, activation, int(bool(gated)), z,
             ldz, d, lddz, da, ldda, db, lddb, stride_db, dbv, w, wb)
