@@ -197,7 +197,7 @@ int moe_plan(int64_t choices, int64_t experts, const int32_t* ids, int32_t* offs
     const hipStream_t s = static_cast<hipStream_t>(stream);
     (void)hipGetLastError();
     if (chunks > 1) {
-        hipLaunchKernelGGL(tgemm::plan_count, dim3((unsigned)chunks), dim3(256), 0, s, p);
+        hipLaunchKernelGGL(tgemm::plan_count, dim3((unsigned)chunks), dim3(1024), 0, s, p);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess)
             return status(e);

@@ -25,41 +25,63 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
 // wave's LDS accesses in order, the compiler is kept from moving them.
 __device__ __forceinline__ void wave_lds_sync() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
-// Reductions over the 64 lanes of a wave, the result in every lane.  fp32: four rotations
-// within rows of 16 lanes and two swaps of rows, all in vector registers; fp64 (the rare
-// exact path): shuffles.
+// Reductions over the 64 lanes of a wave, the result in every lane: four rotations within
+// rows of 16 lanes and two swaps of rows, all in vector registers (a shuffle through LDS
+// takes five times as long).
+template <int CTRL>
+__device__ __forceinline__ uint32_t row_rotate(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false);
+}
 template <int CTRL>
 __device__ __forceinline__ float row_rotate(float v) {
-    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, false));
+    return __uint_as_float(row_rotate<CTRL>(__float_as_uint(v)));
 }
-template <typename OP>
-__device__ __forceinline__ float wave_all(float v, OP&& op) {
+template <int CTRL>
+__device__ __forceinline__ double row_rotate(double v) {
+    const uint64_t u = (uint64_t)__double_as_longlong(v);
+    const uint64_t lo = row_rotate<CTRL>((uint32_t)u), hi = row_rotate<CTRL>((uint32_t)(u >> 32));
+    return __longlong_as_double((long long)(lo | hi << 32));
+}
+// The value with odd and even rows of 16 lanes (ROWS 16) or the two halves (ROWS 32) paired
+// up: both members of the pair, in every lane.
+template <int ROWS>
+__device__ __forceinline__ u32x2 swap_rows(uint32_t v) {
+    if constexpr (ROWS == 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        return u32x2{r[0], r[1]};
+    } else {
+        const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        return u32x2{r[0], r[1]};
+    }
+}
+template <int ROWS, typename OP>
+__device__ __forceinline__ float over_rows(float v, OP&& op) {
+    const u32x2 r = swap_rows<ROWS>(__float_as_uint(v));
+    return op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+template <int ROWS, typename OP>
+__device__ __forceinline__ double over_rows(double v, OP&& op) {
+    const uint64_t u = (uint64_t)__double_as_longlong(v);
+    const u32x2 lo = swap_rows<ROWS>((uint32_t)u), hi = swap_rows<ROWS>((uint32_t)(u >> 32));
+    return op(__longlong_as_double((long long)((uint64_t)lo[0] | (uint64_t)hi[0] << 32)),
+              __longlong_as_double((long long)((uint64_t)lo[1] | (uint64_t)hi[1] << 32)));
+}
+template <typename T, typename OP>
+__device__ __forceinline__ T wave_all(T v, OP&& op) {
     v = op(v, row_rotate<0x128>(v));
     v = op(v, row_rotate<0x124>(v));
     v = op(v, row_rotate<0x122>(v));
     v = op(v, row_rotate<0x121>(v));
-    auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = op(__uint_as_float(r[0]), __uint_as_float(r[1]));
-    r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    return op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    v = over_rows<16>(v, op);
+    return over_rows<32>(v, op);
 }
-__device__ __forceinline__ float wave_max(float v) {
-    return wave_all(v, [](float a, float b) { return fmaxf(a, b); });
+template <typename T>
+__device__ __forceinline__ T wave_max(T v) {
+    return wave_all(v, [](T a, T b) { return a > b ? a : b; });
 }
-__device__ __forceinline__ float wave_sum(float v) {
-    return wave_all(v, [](float a, float b) { return a + b; });
-}
-__device__ __forceinline__ double wave_max(double v) {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2)
-        v = fmax(v, __shfl_xor(v, d));
-    return v;
-}
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2)
-        v += __shfl_xor(v, d);
-    return v;
+template <typename T>
+__device__ __forceinline__ T wave_sum(T v) {
+    return wave_all(v, [](T a, T b) { return a + b; });
 }
 __device__ __forceinline__ float lane_value(float v, int lane) {
     return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
@@ -565,20 +587,23 @@ __device__ __forceinline__ int plan_expert(const PlanArgs& p, int64_t i) {
     return e >= 0 && e < p.experts ? e : -1;
 }
 
-static __global__ void __launch_bounds__(256) plan_count(const PlanArgs p) {
+static __global__ void __launch_bounds__(1024) plan_count(const PlanArgs p) {
     __shared__ int count[kMaxExperts];
-    for (int e = (int)threadIdx.x; e < p.experts; e += 256)
-        count[e] = 0;
+    const int tid = (int)threadIdx.x;
+    int e[kPlanChunk / 1024];
+#pragma unroll
+    for (int q = 0; q < kPlanChunk / 1024; ++q)
+        e[q] = plan_expert(p, (int64_t)blockIdx.x * kPlanChunk + q * 1024 + tid);
+    if (tid < p.experts)
+        count[tid] = 0;
     __syncthreads();
-    const int64_t first = (int64_t)blockIdx.x * kPlanChunk;
-    for (int i = (int)threadIdx.x; i < kPlanChunk; i += 256) {
-        const int e = plan_expert(p, first + i);
-        if (e >= 0)
-            atomicAdd(&count[e], 1);       // a sum of ones: the order does not matter
-    }
+#pragma unroll
+    for (int q = 0; q < kPlanChunk / 1024; ++q)
+        if (e[q] >= 0)
+            atomicAdd(&count[e[q]], 1);    // a sum of ones: the order does not matter
     __syncthreads();
-    for (int e = (int)threadIdx.x; e < p.experts; e += 256)
-        p.counts[(int64_t)blockIdx.x * p.experts + e] = count[e];
+    if (tid < p.experts)
+        p.counts[(int64_t)blockIdx.x * p.experts + tid] = count[tid];
 }
 
 // CAP: the most experts.
@@ -595,14 +620,20 @@ __global__ void __launch_bounds__(kPlanWaves * 64) plan_place(const PlanArgs p) 
     // this wave's run of choices: whole groups of 64
     const int per_wave = ((n + kPlanWaves * 64 - 1) / (kPlanWaves * 64)) * 64;
     const int w0 = wave * per_wave, w1 = w0 + per_wave < n ? w0 + per_wave : n;
+    constexpr int R = kPlanChunk / (kPlanWaves * 64);   // a lane's choices, at most
+    int mine[R];
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+        const int i = w0 + 64 * q + lane;
+        mine[q] = i < w1 ? plan_expert(p, chunk0 + i) : -1;
+    }
     for (int i = tid; i < kPlanWaves * p.experts; i += kPlanWaves * 64)
         waves[i] = 0;
     __syncthreads();
-    for (int i = w0 + lane; i < w1; i += 64) {
-        const int e = plan_expert(p, chunk0 + i);
-        if (e >= 0)
-            atomicAdd(&waves[wave * p.experts + e], 1);
-    }
+#pragma unroll
+    for (int q = 0; q < R; ++q)
+        if (mine[q] >= 0)
+            atomicAdd(&waves[wave * p.experts + mine[q]], 1);
     __syncthreads();
     // each expert's choices: in all, before this chunk, and before each wave of it
     int all = 0, before = 0;
@@ -616,7 +647,7 @@ __global__ void __launch_bounds__(kPlanWaves * 64) plan_place(const PlanArgs p) 
         all = here;
         if (p.chunks > 1) {
             all = 0;
-#pragma unroll 8
+#pragma unroll 16
             for (int b = 0; b < p.chunks; ++b) {
                 const int c = p.counts[(int64_t)b * p.experts + tid];
                 before += b < (int)blockIdx.x ? c : 0;
@@ -649,9 +680,11 @@ __global__ void __launch_bounds__(kPlanWaves * 64) plan_place(const PlanArgs p) 
     __syncthreads();
     // the rows, 64 choices at a time; the wave's count of an expert moves on by the lanes
     // that hold it (a wave's LDS accesses complete in order)
-    for (int i0 = w0; i0 < w1; i0 += 64) {
-        const int i = i0 + lane;
-        const int e = i < w1 ? plan_expert(p, chunk0 + i) : -1;
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+        const int i = w0 + 64 * q + lane, e = mine[q];
+        if (w0 + 64 * q >= w1)
+            break;
         const unsigned long long same = equal_lanes(e, p.experts);
         int r = -1;
         if (e >= 0) {
