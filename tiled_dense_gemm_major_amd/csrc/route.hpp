@@ -124,8 +124,8 @@ __device__ __forceinline__ uint32_t ordered(float v) {
 //   The fp32 choice: a search over the lanes' largest values (one ballot per step) finds a
 //   bound that a few more than k values reach; those go to LDS, one per lane, and each
 //   counts the ones before it.  Rounds that take one largest value after the other cost
-//   three times the instructions (52 -> the time in the table of the design notes for
-//   16384 tokens, 256 experts in 8 groups); they remain where more than 64 values reach the
+//   three times the instructions (16384 tokens, 256 experts in 8 groups: 52 us so, 27 by the
+//   search, whose 588 vector instructions a token are what bounds it); they remain where more than 64 values reach the
 //   bound (ties), and in fp64.
 struct RouteArgs {
     const void* x;
@@ -466,6 +466,7 @@ __global__ void __launch_bounds__(256) route_tokens(const RouteArgs p) {
 //   logistic               dx_e = [e chosen] g_e s_e (1 - s_e)
 //   logistic, renormalized dx_e = [e chosen] w'_e (1 - s_e) (g_e - sum_j g_j w'_j)
 // One wave per token, everything in fp32; choices outside the experts are passed over.
+// 8192 tokens of 128 experts in bf16: 6.6 us, 275 vector instructions a token.
 // ------------------------------------------------------------------------------------
 struct RouteGradArgs {
     const void* x;
@@ -555,6 +556,7 @@ __global__ void __launch_bounds__(256) route_grad(const RouteGradArgs p) {
 // ranks follow the order of the choices whatever the schedule.  Up to kPlanChunk choices
 // one workgroup does all of it; beyond, plan_count writes the count of each chunk of
 // choices and plan_place, one workgroup per chunk, adds up the chunks before its own.
+// Bound by latency: 131072 choices of 256 experts 3.8 + 8.6 us, 64 of 64 3.3 us.
 // ------------------------------------------------------------------------------------
 constexpr int kPlanChunk = 4096, kPlanWaves = 16;   // one workgroup's choices, its waves
 
@@ -707,7 +709,8 @@ __global__ void __launch_bounds__(kPlanWaves * 64) plan_place(const PlanArgs p) 
 // ------------------------------------------------------------------------------------
 // The combination: Y[t] = residual[t] + sum_j w[t,j] O[slot[t,j]], summed in fp32 in the
 // order of j and rounded once.  A thread owns eight columns of a token; the k rows' loads
-// are independent of each other.  Bound by memory.
+// are independent of each other.  Bound by memory: 4096 tokens of 8 rows of 2048 in 29 us,
+// 5.7 TB/s.
 // ------------------------------------------------------------------------------------
 struct CombineArgs {
     const u16* O;
@@ -765,7 +768,7 @@ __global__ void __launch_bounds__(256) combine_rows(const CombineArgs p) {
 
 // Its backward pass: dO[slot[t,j]] = w[t,j] dY[t] and dw[t,j] = <dY[t], O[slot[t,j]]>, one
 // wave per choice (the waves of a token read the same dY row, from cache), the inner
-// product in fp32.  A choice without a row has dw 0.
+// product in fp32.  A choice without a row has dw 0.  1998 choices of 1024 in 6.3 us.
 struct CombineGradArgs {
     const u16* dY;
     const u16* O;              // null: dw is not wanted
