@@ -540,3 +540,51 @@ def test_two_streams_at_once(tg):
                 got[i].append(_feed_forward(tg, xs[i], wr, w1, None, w2, k)[0])
     torch.cuda.synchronize()
     assert all(torch.equal(y, want[i]) for i in range(2) for y in got[i])
+
+
+def _pool(pointer):
+    """The stream whose pool an address that torch allocated lies in."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= pointer < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+    raise AssertionError("not torch's memory")
+
+
+@pytest.mark.parametrize("as_int", [False, True])
+def test_memory_of_a_call_on_a_given_stream(tg, monkeypatch, as_int):
+    """What a call allocates comes from the pool of the stream that it runs on: memory of the
+    current stream's pool could be given out again while the kernels still run."""
+    s = torch.cuda.Stream()
+    stream = s.cuda_stream if as_int else s
+    seen = []
+    launch = tg._launch
+
+    def spy(name, t, on, *args):
+        seen.append((name, args))
+        return launch(name, t, on, *args)
+
+    monkeypatch.setattr(tg, "_launch", spy)
+    a, b = eighths((40, 64), 1, torch.bfloat16).cuda(), eighths((96, 64), 2, torch.bfloat16).cuda()
+    like = {"dtype": torch.bfloat16, "device": "cuda"}
+    z, dc = torch.zeros(40, 96, **like), eighths((40, 96), 3, torch.bfloat16).cuda()
+    logits = torch.randn(2100, 8, generator=torch.Generator().manual_seed(4)).cuda()
+    rows, experts = torch.zeros(4200, 16, **like), eighths((8, 32, 16), 5, torch.bfloat16).cuda()
+    torch.cuda.synchronize()
+    made = [tg.gemm_fused(a, b, activation=ACT_RELU, preact=z, stream=stream),
+            *tg.gemm_fused_backward(dc, a, b, z, activation=ACT_RELU, dbias=True, stream=stream)]
+    ids, weights = tg.moe_route(logits, 2, stream=stream)
+    plan = tg.moe_plan(ids, 8, stream=stream)
+    y = tg.moe_combine(rows, plan.slots, weights, stream=stream)
+    made += [ids, weights, *plan, y,
+             *tg.moe_combine_backward(y, rows, plan.slots, weights, stream=stream),
+             tg.moe_route_backward(logits, ids, weights, stream=stream)]
+    out = tg.gemm_grouped(rows, experts, plan.offsets, stream=stream)
+    made += [out, *tg.gemm_grouped_backward(out, rows, experts, plan.offsets, stream=stream)[:2]]
+    s.synchronize()
+    assert [_pool(t.data_ptr()) for t in made] == [s.cuda_stream] * len(made)
+    calls = dict(seen)
+    # the gradient of z and the workspaces, which only the call holds
+    hidden = [calls["gemm_fused_backward"][15], calls["gemm_fused_backward"][-2],
+              calls["moe_plan"][-2]]
+    assert all(hidden)
+    assert [_pool(p) for p in hidden] == [s.cuda_stream] * len(hidden)

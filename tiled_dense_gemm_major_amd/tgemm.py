@@ -345,8 +345,11 @@ def gemm(A, B, C=None, b_layout=B_NK, config: Config | None = None, stream=None)
 # Matrices are 2-D tensors whose last dimension is contiguous; the row stride is free.  All
 # tensors of a call lie on one GPU, which need not be the current one; the work goes to the
 # given stream, or to the current stream of that GPU.  Outputs may be passed in; those that
-# are not are allocated by torch.  Nothing here is differentiable by itself: the gradients
-# are calls of their own.
+# are not, and workspaces, are allocated by torch in the pool of the stream that the work
+# goes to, so that their memory is not given out again before the work is done.  Tensors
+# passed to a call on another stream than their own are the caller's to keep, as for any
+# other use on a second stream.  Nothing here is differentiable by itself: the gradients are
+# calls of their own.
 
 def _matrix(t, what, like=None, shape=None):
     """(address, rows, columns, row stride) of a 2-D tensor, after its checks."""
@@ -396,6 +399,18 @@ def _operand_dtype(t, what):
     if not t.is_cuda:
         raise ValueError(f"{what} must be on a GPU, not on {t.device}")
     return halves[t.dtype]
+
+
+def _new(like, shape, stream, dtype=None):
+    """An uninitialised tensor on like's GPU, in the pool of the given stream (None: the
+    current one)."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    cuda = _torch()[0].cuda
+    if isinstance(stream, int):
+        stream = cuda.ExternalStream(stream, device=like.device)
+    with cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _launch(name, t, stream, *args):
@@ -457,7 +472,7 @@ def gemm_fused(A, B, C=None, b_layout=B_NK, bias=None, activation=ACT_NONE, gate
     n, _ = _b_sizes(B, b_layout, k)
     width = _width(n, gated)
     if C is None:
-        C = A.new_empty((m, width))
+        C = _new(A, (m, width), stream)
     c, _, _, ldc = _matrix(C, "C", A, (m, width))
     e = _epilogue(A, m, n, width, activation, gated, bias, residual, preact)
     _launch("gemm_fused", A, stream, dtype, m, n, k, a, lda, b, ldb, b_layout, c, ldc, e)
@@ -474,15 +489,15 @@ def backward_workspace_size(rows, n, k=0, groups=1, dbias=True) -> int:
     return int(nbytes.value)
 
 
-def _gradient(t, like, shape, dtype=None):
+def _gradient(t, like, shape, stream, dtype=None):
     """An output that is wanted (a tensor, or True to allocate it) or not (None, False)."""
     if t is None or t is False:
         return None
-    return like.new_empty(shape, dtype=dtype or like.dtype) if t is True else t
+    return _new(like, shape, stream, dtype) if t is True else t
 
 
 def _gradient_buffers(A, rows, n, k, groups, activation, gated, preact, dZ, dA, dB, dbias,
-                      workspace):
+                      workspace, stream):
     """(preact address and stride, dZ address and stride, workspace address and bytes)."""
     z = zs = d = ds = w = wb = 0
     if activation or gated:
@@ -491,12 +506,12 @@ def _gradient_buffers(A, rows, n, k, groups, activation, gated, preact, dZ, dA, 
         z, _, _, zs = _matrix(preact, "preact", A, (rows, n))
         if dA is not None or dB is not None:
             if dZ is None:
-                dZ = A.new_empty((rows, n))
+                dZ = _new(A, (rows, n), stream)
             d, _, _, ds = _matrix(dZ, "dZ", A, (rows, n))
     if workspace is None:
         wb = backward_workspace_size(rows, n, 0 if dB is None else k, groups, dbias is not None)
         if wb:
-            workspace = A.new_empty((wb,), dtype=_torch()[0].uint8)
+            workspace = _new(A, (wb,), stream, _torch()[0].uint8)
             w = workspace.data_ptr()
     else:
         if workspace.get_device() != A.get_device() or not workspace.is_contiguous():
@@ -518,13 +533,13 @@ def gemm_fused_backward(dC, A, B, preact=None, b_layout=B_NK, activation=ACT_NON
     b, b_rows, b_cols, ldb = _matrix(B, "B", A)
     n, _ = _b_sizes(B, b_layout, k)
     dc, _, _, lddc = _matrix(dC, "dC", A, (m, _width(n, gated)))
-    dA, dB = _gradient(dA, A, (m, k)), _gradient(dB, A, (b_rows, b_cols))
-    dbias = _gradient(dbias, A, (n,), torch.float32)
+    dA, dB = _gradient(dA, A, (m, k), stream), _gradient(dB, A, (b_rows, b_cols), stream)
+    dbias = _gradient(dbias, A, (n,), stream, torch.float32)
     da, _, _, ldda = (0, 0, 0, 0) if dA is None else _matrix(dA, "dA", A, (m, k))
     db, _, _, lddb = (0, 0, 0, 0) if dB is None else _matrix(dB, "dB", A, (b_rows, b_cols))
     dbv = 0 if dbias is None else _vector(dbias, "dbias", A, torch.float32, n)
     z, ldz, d, lddz, w, wb, keep = _gradient_buffers(
-        A, m, n, k, 1, activation, gated, preact, dZ, dA, dB, dbias, workspace)
+        A, m, n, k, 1, activation, gated, preact, dZ, dA, dB, dbias, workspace, stream)
     _launch("gemm_fused_backward", A, stream, dtype, m, n, k, dc, lddc, a, lda, b, ldb, b_layout,
             activation, int(bool(gated)), z, ldz, d, lddz, da, ldda, db, lddb, dbv, w, wb)
     return dA, dB, dbias
@@ -569,7 +584,7 @@ def gemm_grouped(A, B, offsets, C=None, row_index=None, row_div=1, b_layout=B_NK
     width, groups = _width(n, gated), B.shape[0]
     rows, off, idx = _groups(A, B, offsets, row_index, row_div)
     if C is None:
-        C = A.new_empty((rows, width))
+        C = _new(A, (rows, width), stream)
     c, _, _, ldc = _matrix(C, "C", A, (rows, width))
     e = _epilogue(A, rows, n, width, activation, gated, bias, residual, preact, groups)
     _launch("gemm_grouped", A, stream, dtype, groups, rows, n, k, off, idx, row_div, a, a_rows,
@@ -590,13 +605,13 @@ def gemm_grouped_backward(dC, A, B, offsets, preact=None, row_index=None, row_di
     groups, b_shape = B.shape[0], tuple(B.shape)
     rows, off, idx = _groups(A, B, offsets, row_index, row_div)
     dc, _, _, lddc = _matrix(dC, "dC", A, (rows, _width(n, gated)))
-    dA, dB = _gradient(dA, A, (rows, k)), _gradient(dB, A, b_shape)
-    dbias = _gradient(dbias, A, (groups, n), torch.float32)
+    dA, dB = _gradient(dA, A, (rows, k), stream), _gradient(dB, A, b_shape, stream)
+    dbias = _gradient(dbias, A, (groups, n), stream, torch.float32)
     da, _, _, ldda = (0, 0, 0, 0) if dA is None else _matrix(dA, "dA", A, (rows, k))
     db, lddb, stride_db = (0, 0, 0) if dB is None else _stack(dB, "dB", A, b_shape)
     dbv = 0 if dbias is None else _vector(dbias, "dbias", A, torch.float32, groups * n)
     z, ldz, d, lddz, w, wb, keep = _gradient_buffers(
-        A, rows, n, k, groups, activation, gated, preact, dZ, dA, dB, dbias, workspace)
+        A, rows, n, k, groups, activation, gated, preact, dZ, dA, dB, dbias, workspace, stream)
     _launch("gemm_grouped_backward", A, stream, dtype, groups, rows, n, k, off, idx, row_div, dc,
             lddc, a, a_rows, lda, b, ldb, stride_b, b_layout, activation, int(bool(gated)), z,
             ldz, d, lddz, da, ldda, db, lddb, stride_db, dbv, w, wb)
@@ -622,9 +637,9 @@ def moe_route(logits, k, scoring=SCORE_SOFTMAX, bias=None, groups=1, topk_groups
     torch = _torch()[0]
     dtype, x, tokens, experts, ldx = _logits(logits)
     if ids is None:
-        ids = logits.new_empty((tokens, k), dtype=torch.int32)
+        ids = _new(logits, (tokens, k), stream, torch.int32)
     if weights is None:
-        weights = logits.new_empty((tokens, k), dtype=torch.float32)
+        weights = _new(logits, (tokens, k), stream, torch.float32)
     i = _vector(ids, "ids", logits, torch.int32, tokens * k)
     w = _vector(weights, "weights", logits, torch.float32, tokens * k)
     bv = 0 if bias is None else _vector(bias, "bias", logits, torch.float32, experts)
@@ -644,7 +659,7 @@ def moe_route_backward(logits, ids, dweights, scoring=SCORE_SOFTMAX, renormalize
     i = _vector(ids, "ids", logits, torch.int32, tokens * k)
     dw = _vector(dweights, "dweights", logits, torch.float32, tokens * k)
     if dlogits is None:
-        dlogits = logits.new_empty((tokens, experts))
+        dlogits = _new(logits, (tokens, experts), stream)
     dx, _, _, lddx = _matrix(dlogits, "dlogits", logits, (tokens, experts))
     _launch("moe_route_backward", logits, stream, dtype, tokens, experts, k, x, ldx, i, dw,
             scoring, int(bool(renormalize)), scale, dx, lddx)
@@ -672,13 +687,13 @@ def moe_plan(ids, experts, offsets=None, order=None, slots=None, workspace=None,
     count = ids.numel()
     i = _vector(ids, "ids", ids, torch.int32, count)
     if offsets is None:
-        offsets = ids.new_empty((experts + 1,))
+        offsets = _new(ids, (experts + 1,), stream)
     if order is None:
-        order = ids.new_empty((count,))
+        order = _new(ids, (count,), stream)
     if slots is None:
-        slots = ids.new_empty(ids.shape)
+        slots = _new(ids, ids.shape, stream)
     if workspace is None and count > 4096:
-        workspace = ids.new_empty((plan_workspace_size(count, experts) // 4,))
+        workspace = _new(ids, (plan_workspace_size(count, experts) // 4,), stream)
     w = wb = 0
     if workspace is not None:
         if workspace.get_device() != ids.get_device() or not workspace.is_contiguous():
@@ -704,7 +719,7 @@ def moe_combine(O, slots, weights=None, residual=None, Y=None, stream=None):
     s = _vector(slots, "slots", O, torch.int32, tokens * k)
     w = 0 if weights is None else _vector(weights, "weights", O, torch.float32, tokens * k)
     if Y is None:
-        Y = O.new_empty((tokens, width))
+        Y = _new(O, (tokens, width), stream)
     y, _, _, ldy = _matrix(Y, "Y", O, (tokens, width))
     r, _, _, ldr = (0, 0, 0, 0) if residual is None else _matrix(residual, "residual", O,
                                                                 (tokens, width))
@@ -714,7 +729,7 @@ def moe_combine(O, slots, weights=None, residual=None, Y=None, stream=None):
 
 def moe_combine_backward(dY, O, slots, weights=None, dO=True, dweights=True, stream=None):
     """(dO, dweights) of moe_combine: dO[slots[t,j]] = weights[t,j] dY[t] (rows that no slot
-    names keep what they held), dweights[t,j] = <dY[t], O[slots[t,j]]> in fp32.  Either:
+    names keep what they held; each row is to be named at most once), dweights[t,j] = <dY[t], O[slots[t,j]]> in fp32.  Either:
     True (allocated), a tensor to fill, or None / False (not wanted)."""
     torch = _torch()[0]
     dtype = _operand_dtype(O, "O")
@@ -725,8 +740,8 @@ def moe_combine_backward(dY, O, slots, weights=None, dO=True, dweights=True, str
     dy, _, _, lddy = _matrix(dY, "dY", O, (tokens, width))
     s = _vector(slots, "slots", O, torch.int32, tokens * k)
     w = 0 if weights is None else _vector(weights, "weights", O, torch.float32, tokens * k)
-    dO = _gradient(dO, O, (rows, width))
-    dweights = _gradient(dweights, O, (tokens, k), torch.float32)
+    dO = _gradient(dO, O, (rows, width), stream)
+    dweights = _gradient(dweights, O, (tokens, k), stream, torch.float32)
     do, _, _, lddo = (0, 0, 0, 0) if dO is None else _matrix(dO, "dO", O, (rows, width))
     dw = 0 if dweights is None else _vector(dweights, "dweights", O, torch.float32, tokens * k)
     _launch("moe_combine_backward", O, stream, dtype, tokens, k, width, dy, lddy, o, rows, ldo, s,
