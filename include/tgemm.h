@@ -330,8 +330,8 @@ int attn_fwd_f16(int64_t batch, int64_t seq, int64_t heads, int64_t dim, const v
  *
  * in fp32 up to one rounding of C (and of z, where it is kept).  The conventions of the
  * products hold (ownership, asynchrony, errors, thread safety), with these differences:
- *   - sizes and leading dimensions are below 2^31; no product of them is bounded (C may
- *     span more than 2^31 elements);
+ *   - rows, N and K are at most 2^31 - 512, leading dimensions below 2^31; no product of
+ *     them is bounded (C may span more than 2^31 elements);
  *   - any 2-byte alignment, size and leading dimension is accepted; the fast kernels need
  *     A and B 16-byte aligned, lda and ldb multiples of 8, K a multiple of 8 (with B
  *     [K,N]: N, and gated N/2, as well) and B (one group's) within 2^31 bytes;

@@ -211,3 +211,24 @@ def test_binding_refuses_what_it_cannot_pass():
         tgemm._matrix(h, "t", h.bfloat16())
     with pytest.raises(ValueError):
         tgemm._width(7, True)
+
+
+@pytest.mark.parametrize("name", ["m", "n", "k"])
+def test_sizes_whose_tiles_would_pass_32_bits(lib, name):
+    """A tile's last row, column or k past a size of 2^31 - 512 could not be told in 32 bits."""
+    far = 1 << 45                      # the pretend tensors' spans do not overlap
+    wide = dict(A=FAKE, B=FAKE + far, C=FAKE + 2 * far, m=8, n=8, k=8, lda=8, ldb=8, ldc=8)
+    ld = {"m": (), "n": ("ldc",), "k": ("lda", "ldb")}[name]
+    for size in ((1 << 31) - 511, (1 << 31) - 1):
+        assert _fused(lib, **{**wide, name: size, **{x: size for x in ld}}) == UNSUPPORTED
+        # told before anything about the pointers
+        assert _fused(lib, **{**wide, name: size, **{x: size for x in ld}, "A": None}) == UNSUPPORTED
+    assert _fused(lib, **{**wide, name: (1 << 31) - 512, **{x: (1 << 31) - 512 for x in ld}, "A": None}) == NULL
+    grouped = {"m": "rows"}.get(name, name)
+    size = (1 << 31) - 511
+    assert _grouped(lib, **{**dict(n=8, k=8, lda=8, ldb=8, ldc=8, stride=1 << 36, a_rows=size), grouped: size,
+                            **{x: size for x in ld}}) == UNSUPPORTED
+    out = ctypes.c_int64(-1)
+    sizes = {"m": 8, "n": 8, "k": 8, name: size}
+    assert lib.gemm_backward_workspace_size(1, sizes["m"], sizes["n"], sizes["k"], 1, ctypes.byref(out)) == UNSUPPORTED
+    assert out.value == -1

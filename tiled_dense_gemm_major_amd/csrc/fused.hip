@@ -49,6 +49,9 @@ using tgemm_fused::SlopeArgs;
 using tgemm_fused::SumArgs;
 
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
+// Rows, N and K: a tile that starts inside ends below 2^31, so that the kernels' 32-bit
+// indexes past a tensor's end compare as such.
+constexpr int64_t kMaxSize = (int64_t(1) << 31) - 512;
 constexpr int64_t kMaxStride = int64_t(1) << 40;   // elements between groups
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -104,7 +107,7 @@ int check_layer(const Layer& l) {
         return TGEMM_ERR_INVALID_VALUE;
     if (l.gated && l.n % 2 != 0)
         return TGEMM_ERR_INVALID_VALUE;
-    if (l.groups > 65535 || l.rows > kMaxDim || l.n > kMaxDim || l.k > kMaxDim ||
+    if (l.groups > 65535 || l.rows > kMaxSize || l.n > kMaxSize || l.k > kMaxSize ||
         l.a_rows > kMaxDim || l.row_div > kMaxDim)
         return TGEMM_ERR_UNSUPPORTED;
     if (l.lda < 1 || l.lda < l.k || l.ldb < 1 || l.ldb < l.b_cols() || l.stride_b < 0)
@@ -600,7 +603,7 @@ int gemm_backward_workspace_size(int64_t groups, int64_t rows, int64_t n, int64_
         return TGEMM_ERR_NULL_POINTER;
     if (groups < 1 || rows < 0 || n < 0 || k < 0 || (dbias != 0 && dbias != 1))
         return TGEMM_ERR_INVALID_VALUE;
-    if (groups > 65535 || rows > kMaxDim || n > kMaxDim || k > kMaxDim)
+    if (groups > 65535 || rows > kMaxSize || n > kMaxSize || k > kMaxSize)
         return TGEMM_ERR_UNSUPPORTED;
     const int64_t sums = dbias ? cdiv(4 * most_slices(groups, rows) * n, 16) * 16 : 0;
     // the parts' sums, for whichever of the forms a call may choose from
