@@ -401,16 +401,68 @@ __device__ __forceinline__ int b_row_of(const FusedArgs& p, int tn, int c) {
 }
 
 // ------------------------------------------------------------------------------------
-// The generic kernel: any alignment, size and layout.  64 x 64 tile, K step 16, four
-// waves of one 32 x 32 MFMA block each, masked loads of single elements into one LDS
-// stage; C through an fp32 tile in LDS.  Bound by its single-element loads: 133 TFLOP/s at
-// 8192 x 8192 x 4097 (bf16, [N,K]), 30 at 1000 x 1000 x 1001.
+// The generic kernel: any alignment, size and layout.  64 x 64 tile, K step 64, four
+// waves of one 32 x 32 MFMA block each; C through an fp32 tile in the same LDS.
+//   Elements are loaded singly, a wave's 64 lanes along the contiguous dimension (whole
+// 128-byte pieces): 32 loads per lane and step, those of the next step in flight beside the
+// MFMAs.  An operand whose k is not the contiguous dimension is turned in registers: a
+// lane's 16 k of one column go to LDS in two 16-byte writes.
 // ------------------------------------------------------------------------------------
+constexpr int kGenericStep = 64, kGenericRow = kGenericStep + 8;   // k per step; LDS row (odd 16-byte pieces)
+
+// Element `at` (in: it lies in the rows) of sixteen rows, the i-th held by lane i of `mine`
+// (< 0: a row of zeros).  Called by whole waves.
+__device__ __forceinline__ void load_rows(u16 (&v)[16], const u16* base, int64_t ld, int mine, int64_t at, bool in) {
+    int row[16];           // read while all lanes are active
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        row[i] = __builtin_amdgcn_readlane(mine, i);
+        v[i] = 0;
+    }
+    if (in) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (row[i] >= 0)
+                v[i] = base[row[i] * ld + at];
+    }
+}
+
+// Lane l's values are k = 16 wave + i of column l.
+__device__ __forceinline__ void put_turned(u16* lds, int lane, int wave, const u16 (&v)[16]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        u32x4 w;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            w[q] = (uint32_t)v[8 * h + 2 * q] | (uint32_t)v[8 * h + 2 * q + 1] << 16;
+        *reinterpret_cast<u32x4*>(lds + lane * kGenericRow + wave * 16 + 8 * h) = w;
+    }
+}
+
+// Lane l's values are k = l of rows 16 wave + i.
+__device__ __forceinline__ void put_rows(u16* lds, int lane, int wave, const u16 (&v)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        lds[(wave * 16 + i) * kGenericRow + lane] = v[i];
+}
+
+template <int DT>
+__device__ __forceinline__ void generic_step(f32x16& acc, const u16* left, const u16* right, int lane, int wm, int wn) {
+#pragma unroll
+    for (int s = 0; s < kGenericStep / 16; ++s) {
+        const int at = (lane & 31) * kGenericRow + 16 * s + (lane >> 5) * 8;
+        const u32x4 lf = *reinterpret_cast<const u32x4*>(left + wm * 32 * kGenericRow + at);
+        const u32x4 rf = *reinterpret_cast<const u32x4*>(right + wn * 32 * kGenericRow + at);
+        acc = mfma_32x32x16<DT>(rf, lf, acc);
+    }
+}
+
 template <int DT, int LAYOUT>
 __global__ void __launch_bounds__(256) fused_generic(const FusedArgs p, int grid_n) {
-    __shared__ __attribute__((aligned(16))) u16 As[64 * 16];
-    __shared__ __attribute__((aligned(16))) u16 Bs[64 * 16];
-    __shared__ __attribute__((aligned(16))) float Cs[64 * 68];
+    __shared__ __attribute__((aligned(16))) u16 lds[2 * 64 * kGenericRow];
+    u16 *const As = lds, *const Bs = lds + 64 * kGenericRow;
+    float* const Cs = reinterpret_cast<float*>(lds);        // [64][68]
+    static_assert(64 * 68 * sizeof(float) <= sizeof(lds), "C staging fits the operands' stage");
     int g, row0, row_end, tn;
     if (!find_tile<64>(p, (int)blockIdx.x, grid_n, 8, g, row0, row_end, tn))
         return;
@@ -418,31 +470,31 @@ __global__ void __launch_bounds__(256) fused_generic(const FusedArgs p, int grid
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int wm = wave >> 1, wn = wave & 1;
     f32x16 acc = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-    // the four A rows and B rows (or, B [K,N], the one column) that this thread loads
-    int ar[4], br[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = (tid + 256 * i) >> 4;
-        ar[i] = row0 + r < row_end ? a_row_of(p, row0 + r) : -1;
-        br[i] = b_row_of<64>(p, tn, LAYOUT == LAYOUT_NK ? r : tid & 63);
-    }
-    for (int k0 = 0; k0 < p.K; k0 += 16) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int e = tid + 256 * i;
-            const int gk = k0 + (e & 15);
-            As[e] = ar[i] >= 0 && gk < p.K ? p.A[(int64_t)ar[i] * p.lda + gk] : (u16)0;
-            if constexpr (LAYOUT == LAYOUT_NK) {
-                Bs[e] = br[i] >= 0 && gk < p.K ? B[(int64_t)br[i] * p.ldb + gk] : (u16)0;
-            } else {
-                const int kk = e >> 6, bk = k0 + kk;
-                Bs[(e & 63) * 16 + kk] = br[i] >= 0 && bk < p.K ? B[(int64_t)bk * p.ldb + br[i]] : (u16)0;
-            }
+    // lane i < 16: the A row and the B row that the wave loads i-th; B [K,N]: the lane's column
+    const int slot = wave * 16 + (lane & 15);
+    const int a_row = row0 + slot < row_end ? a_row_of(p, row0 + slot) : -1;
+    const int b_row = b_row_of<64>(p, tn, LAYOUT == LAYOUT_NK ? slot : lane);
+    u16 av[16], bv[16];
+    auto load = [&](int k0) {
+        load_rows(av, p.A, p.lda, a_row, (int64_t)k0 + lane, lane < p.K - k0);
+        if constexpr (LAYOUT == LAYOUT_NK) {
+            load_rows(bv, B, p.ldb, b_row, (int64_t)k0 + lane, lane < p.K - k0);
+        } else {
+            const int k = k0 + slot;
+            load_rows(bv, B, p.ldb, slot < p.K - k0 ? k : -1, b_row, b_row >= 0);
         }
+    };
+    load(0);
+    for (int k0 = 0; k0 < p.K; k0 += kGenericStep) {
+        put_rows(As, lane, wave, av);
+        if constexpr (LAYOUT == LAYOUT_NK)
+            put_rows(Bs, lane, wave, bv);
+        else
+            put_turned(Bs, lane, wave, bv);
         __syncthreads();
-        const u32x4 af = *reinterpret_cast<const u32x4*>(&As[(wm * 32 + (lane & 31)) * 16 + (lane >> 5) * 8]);
-        const u32x4 bf = *reinterpret_cast<const u32x4*>(&Bs[(wn * 32 + (lane & 31)) * 16 + (lane >> 5) * 8]);
-        acc = mfma_32x32x16<DT>(bf, af, acc);
+        if (k0 + kGenericStep < p.K)
+            load(k0 + kGenericStep);
+        generic_step<DT>(acc, As, Bs, lane, wm, wn);
         __syncthreads();
     }
 #pragma unroll
@@ -507,8 +559,8 @@ __device__ __forceinline__ int sum_row(const SumArgs& p, bool indexed, int s) {
 
 template <int DT>
 __global__ void __launch_bounds__(256) sum_generic(const SumArgs p, int grid_i, int grid_j) {
-    __shared__ __attribute__((aligned(16))) u16 Ls[64 * 16];
-    __shared__ __attribute__((aligned(16))) u16 Rs[64 * 16];
+    __shared__ __attribute__((aligned(16))) u16 Ls[64 * kGenericRow];
+    __shared__ __attribute__((aligned(16))) u16 Rs[64 * kGenericRow];
     const int per = grid_i * grid_j, g = (int)blockIdx.x / per;
     int ti, tj;
     tile_of((int)blockIdx.x % per, grid_i, grid_j, 8, ti, tj);
@@ -516,27 +568,25 @@ __global__ void __launch_bounds__(256) sum_generic(const SumArgs p, int grid_i, 
     group_rows(p, g, lo, hi);
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int wm = wave >> 1, wn = wave & 1;
-    const int ci = ti * 64 + (tid & 63), cj = tj * 64 + (tid & 63);
+    const int ci = ti * 64 + lane, cj = tj * 64 + lane;
     f32x16 acc = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-    for (int s0 = lo; s0 < hi; s0 += 16) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int kk = (tid >> 6) + 4 * i, s = s0 + kk;
-            u16 l = 0, r = 0;
-            if (s < hi) {
-                const int sl = sum_row(p, p.index_left, s), sr = sum_row(p, p.index_right, s);
-                if (sl >= 0 && ci < p.I)
-                    l = p.left[(int64_t)sl * p.ldl + ci];
-                if (sr >= 0 && cj < p.J)
-                    r = p.right[(int64_t)sr * p.ldr + cj];
-            }
-            Ls[(tid & 63) * 16 + kk] = l;
-            Rs[(tid & 63) * 16 + kk] = r;
-        }
+    u16 lv[16], rv[16];
+    auto load = [&](int s0) {
+        // lane i < 16: the row that the wave loads i-th
+        const int slot = wave * 16 + (lane & 15);
+        const bool in = slot < hi - s0;
+        load_rows(lv, p.left, p.ldl, in ? sum_row(p, p.index_left, s0 + slot) : -1, ci, ci < p.I);
+        load_rows(rv, p.right, p.ldr, in ? sum_row(p, p.index_right, s0 + slot) : -1, cj, cj < p.J);
+    };
+    if (lo < hi)
+        load(lo);
+    for (int s0 = lo; s0 < hi; s0 += kGenericStep) {
+        put_turned(Ls, lane, wave, lv);
+        put_turned(Rs, lane, wave, rv);
         __syncthreads();
-        const u32x4 lf = *reinterpret_cast<const u32x4*>(&Ls[(wm * 32 + (lane & 31)) * 16 + (lane >> 5) * 8]);
-        const u32x4 rf = *reinterpret_cast<const u32x4*>(&Rs[(wn * 32 + (lane & 31)) * 16 + (lane >> 5) * 8]);
-        acc = mfma_32x32x16<DT>(rf, lf, acc);
+        if (s0 + kGenericStep < hi)
+            load(s0 + kGenericStep);
+        generic_step<DT>(acc, Ls, Rs, lane, wm, wn);
         __syncthreads();
     }
     const int i = ti * 64 + wm * 32 + (lane & 31);
