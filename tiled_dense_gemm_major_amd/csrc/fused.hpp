@@ -407,12 +407,16 @@ __device__ __forceinline__ int b_row_of(const FusedArgs& p, int tn, int c) {
 // 128-byte pieces): 32 loads per lane and step, those of the next step in flight beside the
 // MFMAs.  An operand whose k is not the contiguous dimension is turned in registers: a
 // lane's 16 k of one column go to LDS in two 16-byte writes.
+//   Bound by the single-element loads: 316 TFLOP/s at 4096 x 4096 x 4097 (bf16, [N,K]; 115
+// with steps of 16 and nothing in flight), 23 us for 1000 x 1000 x 1001 (66), 80 us for
+// 4 x 8192 x 4097 (275); the sum over 4096 rows to 4097 x 4096 512 us (268 TFLOP/s).
 // ------------------------------------------------------------------------------------
 constexpr int kGenericStep = 64, kGenericRow = kGenericStep + 8;   // k per step; LDS row (odd 16-byte pieces)
 
 // Element `at` (in: it lies in the rows) of sixteen rows, the i-th held by lane i of `mine`
-// (< 0: a row of zeros).  Called by whole waves.
-__device__ __forceinline__ void load_rows(u16 (&v)[16], const u16* base, int64_t ld, int mine, int64_t at, bool in) {
+// (< 0: a row of zeros).  Called by whole waves.  One element to a register: held as 16-bit
+// values they are packed in pairs where they are loaded, which waits for every second load.
+__device__ __forceinline__ void load_rows(uint32_t (&v)[16], const u16* base, int64_t ld, int mine, int64_t at, bool in) {
     int row[16];           // read while all lanes are active
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -428,22 +432,22 @@ __device__ __forceinline__ void load_rows(u16 (&v)[16], const u16* base, int64_t
 }
 
 // Lane l's values are k = 16 wave + i of column l.
-__device__ __forceinline__ void put_turned(u16* lds, int lane, int wave, const u16 (&v)[16]) {
+__device__ __forceinline__ void put_turned(u16* lds, int lane, int wave, const uint32_t (&v)[16]) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         u32x4 w;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-            w[q] = (uint32_t)v[8 * h + 2 * q] | (uint32_t)v[8 * h + 2 * q + 1] << 16;
+            w[q] = v[8 * h + 2 * q] | v[8 * h + 2 * q + 1] << 16;
         *reinterpret_cast<u32x4*>(lds + lane * kGenericRow + wave * 16 + 8 * h) = w;
     }
 }
 
 // Lane l's values are k = l of rows 16 wave + i.
-__device__ __forceinline__ void put_rows(u16* lds, int lane, int wave, const u16 (&v)[16]) {
+__device__ __forceinline__ void put_rows(u16* lds, int lane, int wave, const uint32_t (&v)[16]) {
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-        lds[(wave * 16 + i) * kGenericRow + lane] = v[i];
+        lds[(wave * 16 + i) * kGenericRow + lane] = (u16)v[i];
 }
 
 template <int DT>
@@ -474,7 +478,7 @@ __global__ void __launch_bounds__(256) fused_generic(const FusedArgs p, int grid
     const int slot = wave * 16 + (lane & 15);
     const int a_row = row0 + slot < row_end ? a_row_of(p, row0 + slot) : -1;
     const int b_row = b_row_of<64>(p, tn, LAYOUT == LAYOUT_NK ? slot : lane);
-    u16 av[16], bv[16];
+    uint32_t av[16], bv[16];
     auto load = [&](int k0) {
         load_rows(av, p.A, p.lda, a_row, (int64_t)k0 + lane, lane < p.K - k0);
         if constexpr (LAYOUT == LAYOUT_NK) {
@@ -570,7 +574,7 @@ __global__ void __launch_bounds__(256) sum_generic(const SumArgs p, int grid_i, 
     const int wm = wave >> 1, wn = wave & 1;
     const int ci = ti * 64 + lane, cj = tj * 64 + lane;
     f32x16 acc = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-    u16 lv[16], rv[16];
+    uint32_t lv[16], rv[16];
     auto load = [&](int s0) {
         // lane i < 16: the row that the wave loads i-th
         const int slot = wave * 16 + (lane & 15);
